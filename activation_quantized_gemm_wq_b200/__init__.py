@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_PKG, "libwq.so")
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 
 WQ_OK = 0
 STATUS = {0: "WQ_OK", 1: "WQ_ERR_NULL", 2: "WQ_ERR_SHAPE", 3: "WQ_ERR_ALIGN", 4: "WQ_ERR_ARG",
@@ -67,6 +68,13 @@ _SIGS = {
     "wq_linear_gelu_quant": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P,
                                   _P, _P, _P, _I, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "wq_debug_inject_stall": (_I, [_I, ctypes.c_uint]),
+    "wq_pack_int4_group": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
+    "wq_gemv_w4g": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P]),
+    "wq_kv8_append": (_I, [_P, _P, _L, _L, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I,
+                           _P]),
+    "wq_attn_kv8_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "wq_attn_kv8": (_I, [_P, _L, _I, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                         ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]),
     "wq_device_status": (_I, [ctypes.POINTER(ctypes.c_uint)]),
 }
 
@@ -98,6 +106,17 @@ _BF16 = frozenset({"torch.bfloat16", "torch.int16", "torch.uint16"})
 _F32 = frozenset({"torch.float32"})
 _BYTES = frozenset({"torch.uint8", "torch.int8"})
 _I32 = frozenset({"torch.int32"})
+_I8 = frozenset({"torch.int8"})
+
+
+_type_names = {}
+
+
+def _type_name(dtype):
+    name = _type_names.get(dtype)
+    if name is None:
+        name = _type_names[dtype] = str(dtype)
+    return name
 
 
 def _current_device():
@@ -105,25 +124,44 @@ def _current_device():
     return torch.cuda.current_device()
 
 
-def _ptr(t, name, kinds=None, count=0):
+def _ptr(t, name, kinds=None, count=0, device=None):
     """Device address of tensor `t`, which the C call reads or writes as `count`
     elements of one of the element types `kinds` (None: any type, e.g. the
     workspace).  None passes through: the library decides which pointers may be
-    NULL and returns WQ_ERR_NULL for the others."""
+    NULL and returns WQ_ERR_NULL for the others.  device: the current device, where
+    the caller has already asked for it."""
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError(f"{name}: libwq takes device tensors")
     if not t.is_contiguous():
         raise ValueError(f"{name}: libwq takes contiguous tensors")
-    if kinds is not None and str(t.dtype) not in kinds:
+    _check(t, name, kinds, count, device)
+    return t.data_ptr()
+
+
+def _check(t, name, kinds, count, device):
+    if kinds is not None and _type_name(t.dtype) not in kinds:
         raise TypeError(f"{name}: element type {t.dtype}, expected one of {sorted(kinds)}")
     if t.numel() < count:
         raise ValueError(f"{name}: {t.numel()} elements, the call uses {count}")
-    if t.get_device() != _current_device():
+    if t.get_device() != (_current_device() if device is None else device):
         raise ValueError(f"{name}: on cuda:{t.get_device()}, the current device is "
                          f"cuda:{_current_device()}")
-    return t.data_ptr()
+
+
+def _row_ptr(t, name, heads, head_dim, device):
+    """Address and row stride of [rows][heads][head_dim] bf16 rows that may be part of
+    wider ones (a slice of a fused q/k/v projection): packed within a row."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows, {heads}, {head_dim}]")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: libwq takes device tensors")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}: libwq takes rows that are packed within themselves")
+    _check(t, name, _BF16, 0, device)
+    packed = heads * head_dim
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else packed)
 
 
 def _codes_per_row(K, act_bits):
@@ -328,6 +366,95 @@ def wq_linear_gelu_quant(x, cinv, stream_id, alpha, beta, step, act_bits, qw, s_
           act_bits_next, _ptr(codes_next, "codes_next", _BYTES, M * N),
           _ptr(s_next, "s_next", _F32, M), _ptr(h, "h", _BF16, M * N),
           _ptr(workspace, "workspace"), _nbytes(workspace), _stream(stream))
+
+
+def wq_pack_int4_group(W, c, group, qw, s_g, stream=None):
+    """Offline: int4 codes and one bf16 scale per `group` (32, 64 or 128) input channels;
+    qw [N][K/2] (in the layout of include/wq.h), s_g [K/group][N]."""
+    N, K = W.shape
+    dev = _current_device()
+    _call("wq_pack_int4_group", _ptr(W, "W", _BF16, N * K, dev), _ptr(c, "c", _F32, K, dev), N, K,
+          group, _ptr(qw, "qw", _BYTES, N * (K // 2), dev),
+          _ptr(s_g, "s_g", _BF16, _groups(K, group) * N, dev), _stream(stream))
+
+
+def _groups(K, group):
+    return K // group if group > 0 else 0   # a bad group is the library's to refuse
+
+
+def wq_gemv_w4g(x, cinv, qw, s_g, group, bias, y, stream=None):
+    """y = bf16((x * cinv) W'^T + bias) for up to 16 tokens, with the weights of
+    wq_pack_int4_group; cinv and bias may be None."""
+    M, K = x.shape
+    N = qw.shape[0]
+    dev = _current_device()
+    _call("wq_gemv_w4g", _ptr(x, "x", _BF16, M * K, dev), M, K, N, _ptr(cinv, "cinv", _F32, K, dev),
+          _ptr(qw, "qw", _BYTES, N * (K // 2), dev),
+          _ptr(s_g, "s_g", _BF16, _groups(K, group) * N, dev), group,
+          _ptr(bias, "bias", _F32, N, dev), _ptr(y, "y", _BF16, M * N, dev), _stream(stream))
+
+
+def _cache_args(k_codes, v_codes, k_scale, v_scale, block_table, B, dev):
+    """The cache's pointers and sizes, checked: codes [pages][kv_heads][page_tokens][D],
+    scales [pages][kv_heads][page_tokens / 16], block_table [B][max_pages]."""
+    pages, heads, page_tokens, D = k_codes.shape
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table: shape {tuple(block_table.shape)}, expected [{B}, max_pages]")
+    n = pages * heads * page_tokens
+    return (_ptr(block_table, "block_table", _I32, 0, dev), block_table.shape[1],
+            _ptr(k_codes, "k_codes", _I8, n * D, dev), _ptr(v_codes, "v_codes", _I8, n * D, dev),
+            _ptr(k_scale, "k_scale", _F32, n // 16, dev),
+            _ptr(v_scale, "v_scale", _F32, n // 16, dev), pages, heads, page_tokens, D)
+
+
+def wq_kv8_append(k, v, row_start, past_len, block_table, k_codes, v_codes, k_scale, v_scale,
+                  stream=None):
+    """Quantizes new keys and values k, v [T][kv_heads][D] into the paged int8 cache: rows
+    row_start[b] .. row_start[b+1] are the tokens of sequence b from past_len[b] on.  The
+    rows of k and v may be parts of wider ones (a fused q/k/v projection)."""
+    dev = _current_device()
+    B = past_len.shape[0]
+    cache = _cache_args(k_codes, v_codes, k_scale, v_scale, block_table, B, dev)
+    heads, D = cache[-3], cache[-1]
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"v: {v.shape[0]} rows, k has {k.shape[0]}")
+    kp, ks = _row_ptr(k, "k", heads, D, dev)
+    vp, vs = _row_ptr(v, "v", heads, D, dev)
+    _call("wq_kv8_append", kp, vp, ks, vs, k.shape[0],
+          _ptr(row_start, "row_start", _I32, B + 1, dev), _ptr(past_len, "past_len", _I32, B, dev),
+          B, *cache, _stream(stream))
+
+
+def wq_attn_kv8_workspace_bytes(Tq, B, q_heads, kv_heads, head_dim):
+    return int(lib().wq_attn_kv8_workspace_bytes(Tq, B, q_heads, kv_heads, head_dim))
+
+
+def wq_attn_kv8(q, q_start, kv_len, block_table, k_codes, v_codes, k_scale, v_scale, causal, scale,
+                out, lse, workspace, stream=None):
+    """Attention of q [Tq][q_heads][D] over the paged int8 cache: rows q_start[b] ..
+    q_start[b+1] are the queries of sequence b, which sees its kv_len[b] cached tokens, or,
+    with causal, is their last part.  out [Tq][q_heads][D] bf16; lse [Tq][q_heads] fp32 or
+    None.  The rows of q may be parts of wider ones."""
+    dev = _current_device()
+    B = kv_len.shape[0]
+    cache = _cache_args(k_codes, v_codes, k_scale, v_scale, block_table, B, dev)
+    heads, D = q.shape[1], cache[-1]
+    Tq = q.shape[0]
+    qp, qs = _row_ptr(q, "q", heads, D, dev)
+    _call("wq_attn_kv8", qp, qs, Tq, heads, _ptr(q_start, "q_start", _I32, B + 1, dev),
+          _ptr(kv_len, "kv_len", _I32, B, dev), B, *cache, 1 if causal else 0, float(scale),
+          _ptr(out, "out", _BF16, Tq * heads * D, dev), _ptr(lse, "lse", _F32, Tq * heads, dev),
+          _ptr(workspace, "workspace", None, 0, dev), 0 if workspace is None else _nbytes(workspace),
+          _stream(stream))
+
+
+def alloc_attn_workspace(Tq, B, q_heads, kv_heads, head_dim, device="cuda"):
+    """A device workspace for wq_attn_kv8 calls of these sizes (256-byte aligned by torch)."""
+    import torch
+    n = wq_attn_kv8_workspace_bytes(Tq, B, q_heads, kv_heads, head_dim)
+    if n == 0:
+        raise ValueError("invalid sizes for a workspace")
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def wq_debug_inject_stall(enable, limit_us=0):

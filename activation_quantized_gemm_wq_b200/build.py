@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libwq.so")
 SOURCES = ("wq_api.cu",)
-DEPS = ("wq_api.cu", "wq_gemm.cuh", "wq_quant.cuh", "wq_ptx.cuh", "wq_internal.h")
+DEPS = ("wq_api.cu", "wq_gemm.cuh", "wq_quant.cuh", "wq_ptx.cuh", "wq_internal.h",
+        "wq_group.cuh", "wq_kv8.cuh")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

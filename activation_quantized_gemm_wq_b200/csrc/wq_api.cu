@@ -6,8 +6,12 @@
 #include <cstdint>
 #include <mutex>
 
+#include <cmath>
+
 #include "wq_gemm.cuh"
+#include "wq_group.cuh"
 #include "wq_internal.h"
+#include "wq_kv8.cuh"
 #include "wq_quant.cuh"
 
 namespace {
@@ -15,6 +19,8 @@ namespace {
 constexpr size_t kAlign = 256;
 
 size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -29,6 +35,39 @@ wq_status check_n(int N) { return (N < 16 || (N % 16) != 0) ? WQ_ERR_SHAPE : WQ_
 
 wq_status check_table(int S, int T, int step) {
   if (S < 1 || S > 255 || T < 1 || step < 0 || step >= T) return WQ_ERR_ARG;
+  return WQ_OK;
+}
+
+constexpr long long kMaxGrid = 2147483647;
+
+wq_status check_group(int group) {
+  return group == 32 || group == 64 || group == 128 ? WQ_OK : WQ_ERR_ARG;
+}
+
+// A paged cache: the copies' row coordinate (page, head, slot) and a sequence's token
+// positions are 32-bit.
+wq_status check_cache(int B, int max_pages, int pages, int kv_heads, int page_tokens,
+                      int head_dim) {
+  if (B < 0 || max_pages < 1 || pages < 1 || kv_heads < 1) return WQ_ERR_SHAPE;
+  if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128)
+    return WQ_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return WQ_ERR_SHAPE;
+  if (static_cast<long long>(pages) * kv_heads > kMaxGrid / page_tokens) return WQ_ERR_SHAPE;
+  if (max_pages > kMaxGrid / page_tokens - 1) return WQ_ERR_SHAPE;
+  return WQ_OK;
+}
+
+// Rows of heads x head_dim packed elements, `stride` apart, each 16-byte aligned.
+wq_status check_rows(int64_t stride, int heads, int head_dim) {
+  return stride >= static_cast<int64_t>(heads) * head_dim && stride % 8 == 0 ? WQ_OK
+                                                                             : WQ_ERR_SHAPE;
+}
+
+wq_status check_attn(int Tq, int B, int q_heads, int kv_heads, int head_dim) {
+  if (Tq < 0 || B < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0)
+    return WQ_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return WQ_ERR_SHAPE;
+  if (static_cast<long long>(Tq) * q_heads > kMaxGrid) return WQ_ERR_SHAPE;
   return WQ_OK;
 }
 
@@ -460,13 +499,104 @@ wq_status wq_linear_w4a8_noalloc(const wq_bf16* x, int M, int K, int N, const fl
                 need > 0 ? kNoAllocScratchBytes : 0, stream, 8);
 }
 
+wq_status wq_pack_int4_group(const wq_bf16* W, const float* c, int N, int K, int group,
+                             uint8_t* qw, wq_bf16* s_g, wq_stream_t stream) {
+  WQ_TRY(check_group(group));
+  WQ_TRY(check_mk(0, K));
+  if (N < 1 || static_cast<long long>(N) * K / 8 / 256 > kMaxGrid - 1) return WQ_ERR_SHAPE;
+  if (!W || !qw || !s_g) return WQ_ERR_NULL;
+  if (!aligned16(W) || !aligned16(qw) || !aligned(s_g, 2) || (c && !aligned16(c)))
+    return WQ_ERR_ALIGN;
+  return from_cuda(wq::launch_pack_int4_group(W, c, N, K, group, qw, s_g,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
+                      const uint8_t* qw, const wq_bf16* s_g, int group, const float* bias,
+                      wq_bf16* y, wq_stream_t stream) {
+  WQ_TRY(check_group(group));
+  WQ_TRY(check_mk(M, K));
+  if (M > wq::kGemvMaxM || N < 1 || N > kMaxGrid - 64) return WQ_ERR_SHAPE;
+  if (M == 0) return WQ_OK;
+  if (!x || !qw || !s_g || !y) return WQ_ERR_NULL;
+  if (!aligned16(x) || !aligned16(qw) || !aligned(s_g, 2) || !aligned(y, 2) ||
+      (cinv && !aligned16(cinv)) || (bias && !aligned(bias, 4)))
+    return WQ_ERR_ALIGN;
+  return from_cuda(wq::launch_gemv_w4g(x, cinv, qw, s_g, group, bias, y, M, K, N,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+wq_status wq_kv8_append(const wq_bf16* k, const wq_bf16* v, int64_t k_stride, int64_t v_stride,
+                        int T, const int32_t* row_start, const int32_t* past_len, int B,
+                        const int32_t* block_table, int max_pages, int8_t* k_codes,
+                        int8_t* v_codes, float* k_scale, float* v_scale, int pages, int kv_heads,
+                        int page_tokens, int head_dim, wq_stream_t stream) {
+  WQ_TRY(check_cache(B, max_pages, pages, kv_heads, page_tokens, head_dim));
+  if (T < 0) return WQ_ERR_SHAPE;
+  if (T == 0 || B == 0) return WQ_OK;
+  WQ_TRY(check_rows(k_stride, kv_heads, head_dim));
+  WQ_TRY(check_rows(v_stride, kv_heads, head_dim));
+  if ((static_cast<long long>(T) * kv_heads * 2 + 3) / 4 > kMaxGrid) return WQ_ERR_SHAPE;
+  if (!k || !v || !row_start || !past_len || !block_table || !k_codes || !v_codes || !k_scale ||
+      !v_scale)
+    return WQ_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(row_start, 4) ||
+      !aligned(past_len, 4) || !aligned(block_table, 4))
+    return WQ_ERR_ALIGN;
+  const wq::Kv8Append p{k, v, k_stride, v_stride, T, row_start, past_len,
+                        {block_table, B, max_pages, k_codes, v_codes, k_scale, v_scale, pages,
+                         kv_heads, page_tokens, head_dim}};
+  return from_cuda(wq::launch_kv8_append(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t wq_attn_kv8_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int head_dim) {
+  if (check_attn(Tq, B, q_heads, kv_heads, head_dim) != WQ_OK) return 0;
+  return wq::attn_workspace_bytes(Tq, B, q_heads, kv_heads, head_dim);
+}
+
+wq_status wq_attn_kv8(const wq_bf16* q, int64_t q_stride, int Tq, int q_heads,
+                      const int32_t* q_start, const int32_t* kv_len, int B,
+                      const int32_t* block_table, int max_pages, const int8_t* k_codes,
+                      const int8_t* v_codes, const float* k_scale, const float* v_scale,
+                      int pages, int kv_heads, int page_tokens, int head_dim, int causal,
+                      float scale, wq_bf16* out, float* lse, void* workspace, size_t ws_bytes,
+                      wq_stream_t stream) {
+  WQ_TRY(check_attn(Tq, B, q_heads, kv_heads, head_dim));
+  WQ_TRY(check_cache(B, max_pages, pages, kv_heads, page_tokens, head_dim));
+  if (!std::isfinite(scale)) return WQ_ERR_ARG;
+  if (Tq == 0 || B == 0) return WQ_OK;
+  WQ_TRY(check_rows(q_stride, q_heads, head_dim));
+  if (!q || !q_start || !kv_len || !block_table || !k_codes || !v_codes || !k_scale || !v_scale ||
+      !out || !workspace)
+    return WQ_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(out) ||
+      !aligned(workspace, kAlign) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+      !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4) ||
+      (lse && !aligned(lse, 4)))
+    return WQ_ERR_ALIGN;
+  if (ws_bytes < wq::attn_workspace_bytes(Tq, B, q_heads, kv_heads, head_dim)) return WQ_ERR_ARG;
+  const wq::Kv8Attn p{q, q_stride, Tq, q_heads, q_start, kv_len,
+                      {block_table, B, max_pages, const_cast<int8_t*>(k_codes),
+                       const_cast<int8_t*>(v_codes), const_cast<float*>(k_scale),
+                       const_cast<float*>(v_scale), pages, kv_heads, page_tokens, head_dim},
+                      causal != 0, scale, out, lse, workspace};
+  return from_cuda(wq::launch_attn_kv8(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 wq_status wq_device_status(unsigned* flags) {
-  unsigned word = 0;
+  unsigned word = 0, cache_word = 0;
   const unsigned zero = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) return WQ_ERR_CUDA;
   if (cudaMemcpyFromSymbol(&word, wq::g_error_word, sizeof word) != cudaSuccess) return WQ_ERR_CUDA;
   if (word != 0 && cudaMemcpyToSymbol(wq::g_error_word, &zero, sizeof zero) != cudaSuccess)
     return WQ_ERR_CUDA;
+  if (cudaMemcpyFromSymbol(&cache_word, wq::g_cache_error_word, sizeof cache_word) != cudaSuccess)
+    return WQ_ERR_CUDA;
+  if (cache_word != 0 &&
+      cudaMemcpyToSymbol(wq::g_cache_error_word, &zero, sizeof zero) != cudaSuccess)
+    return WQ_ERR_CUDA;
+  word |= cache_word;
   if (flags) *flags = word;
   if (word & WQ_DEVICE_ERR_TIMEOUT) return WQ_ERR_TIMEOUT;
   if (word) return WQ_ERR_DEVICE;

@@ -179,4 +179,47 @@ cudaError_t launch_gemm_gelu_quant(const void* qx, const uint8_t* qw, int M, int
                                    const SplitScratch* scratch, cudaStream_t st, bool w_prefetch,
                                    const GemmExtras& extras);
 
+// ---- int4 weights with group scales, the weight-only product (wq_group.cuh)
+constexpr int kGemvMaxM = 16;
+cudaError_t launch_pack_int4_group(const uint16_t* W, const float* c, int N, int K, int group,
+                                   uint8_t* qw, uint16_t* s_g, cudaStream_t st);
+cudaError_t launch_gemv_w4g(const uint16_t* x, const float* cinv, const uint8_t* qw,
+                            const uint16_t* s_g, int group, const float* bias, uint16_t* y, int M,
+                            int K, int N, cudaStream_t st);
+
+// ---- the paged int8 cache (wq_kv8.cuh)
+struct Kv8Cache {
+  const int* table;  // [B][max_pages]
+  int B, max_pages;
+  int8_t *k_codes, *v_codes;  // [pages][kv_heads][page_tokens][D]
+  float *k_scale, *v_scale;   // [pages][kv_heads][page_tokens / 16]
+  int pages, kv_heads, page_tokens, D;
+};
+
+struct Kv8Append {
+  const uint16_t *k, *v;          // [T] rows of kv_heads x D
+  long long k_stride, v_stride;   // elements between rows
+  int T;
+  const int* row_start;           // [B + 1]
+  const int* past_len;            // [B]
+  Kv8Cache cache;
+};
+cudaError_t launch_kv8_append(const Kv8Append& p, cudaStream_t st);
+
+struct Kv8Attn {
+  const uint16_t* q;  // [Tq] rows of q_heads x D
+  long long q_stride;
+  int Tq, q_heads;
+  const int* q_start;  // [B + 1]
+  const int* kv_len;   // [B]
+  Kv8Cache cache;      // codes and scales are only read
+  int causal;
+  float scale;
+  uint16_t* out;       // [Tq][q_heads][D]
+  float* lse;          // [Tq][q_heads] or null
+  void* workspace;
+};
+size_t attn_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int D);
+cudaError_t launch_attn_kv8(const Kv8Attn& p, cudaStream_t st);
+
 }  // namespace wq

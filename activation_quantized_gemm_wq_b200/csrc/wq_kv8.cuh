@@ -1,0 +1,857 @@
+// A paged key/value cache in int8 and the attention that reads it (the denoiser keeps
+// the keys and values of its context tokens between steps; App. D names the cache).
+//   kv8_append  quantizes new keys and values into the cache
+//   attn_kv8    softmax(scale q k^T) v over the cached tokens
+//
+// Cache: codes int8 [pages][kv_heads][page_tokens][D], scales fp32
+// [pages][kv_heads][page_tokens / 16]: one scale per head and block of 16 tokens, for
+// keys and values each; value = scale * code.  A sequence's token p lies in page
+// table[b][p / page_tokens], slot p % page_tokens; blocks never straddle pages.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "wq_internal.h"
+#include "wq_ptx.cuh"
+#include "wq_quant.cuh"
+
+namespace wq {
+
+// Device error bits of the cache operators.  A word of their own: the GEMM's waits
+// look at g_error_word and would give up on any bit in it.
+enum : unsigned { kErrCache = 4u };
+__device__ unsigned int g_cache_error_word = 0u;
+
+namespace {
+
+constexpr int kBlockTokens = 16;
+
+__device__ __forceinline__ void raise_cache_error() { atomicOr(&g_cache_error_word, kErrCache); }
+
+// The sequence that packed row r belongs to: the last b with start[b] <= r, found 32
+// candidates at a time by a whole warp; -1 if r is before the first or behind the last
+// sequence.  Stays within start[0..B] whatever the values are.
+__device__ __forceinline__ int find_sequence(const int* __restrict__ start, int B, int r) {
+  if (r < start[0] || r >= start[B]) return -1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, span = B;  // the answer lies in [lo, lo + span)
+  while (span > 1) {
+    const int step = (span + 31) / 32;
+    const int at = lo + lane * step;
+    const bool in = lane * step < span;
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, in && start[in ? at : lo] <= r);
+    const int k = hit ? 31 - __clz(hit) : 0;
+    span = min(step, span - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------ append
+
+struct AppendArgs {
+  const uint16_t* x[2];  // keys, values: bf16 rows [T], heads x D packed within a row
+  long long stride[2];   // elements between rows
+  const int* row_start;  // [B + 1]
+  const int* past_len;   // [B]
+  const int* table;      // [B][max_pages]
+  int8_t* codes[2];
+  float* scale[2];
+  int T, B, max_pages, pages, heads, page_tokens;
+  int window;  // packed rows a warp looks through for the first tokens of blocks
+};
+
+// A warp quantizes whole blocks: all new tokens of one block, one head, keys or values.
+// It loads them (at most 16 x D bf16, all loads issued together), takes their maximum by
+// shuffles, and
+//   s_new = max(s_old, max|x| / 127)  (s_old: the block's scale if it has older tokens),
+//   new codes  clamp(rint(x / s_new), +-127),
+//   old codes  rint(code * (s_old / s_new)) when the scale grew,
+// so a block's scale is that of the largest value ever appended to it, however the
+// tokens came.  IEEE fp32 throughout: codes and scales are reproducible bit for bit.
+// A block is handled by the warp whose window holds its first new token; the window is
+// one row for decoding (a warp per new token) and 16 rows for long runs (about one block
+// per warp, and no warps that find nothing).
+template <int D>
+__global__ void __launch_bounds__(128) kv8_append_kernel(const AppendArgs a) {
+  constexpr int TC = D / 8;                        // 8-channel chunks of a token
+  constexpr int CPL = kBlockTokens * TC / 32;      // chunks per lane of a full block
+  const int lane = threadIdx.x & 31;
+  const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int windows = (a.T + a.window - 1) / a.window;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (unit >= static_cast<long long>(windows) * a.heads * 2) return;
+  const int which = static_cast<int>(unit & 1);
+  const int head = static_cast<int>((unit >> 1) % a.heads);
+  const int t0 = static_cast<int>((unit >> 1) / a.heads) * a.window;
+  const int t_end = min(t0 + a.window, a.T);
+  const uint16_t* x = a.x[which];
+  int8_t* codes = a.codes[which];
+  float* scales = a.scale[which];
+  const long long stride = a.stride[which];
+  const long long capacity = static_cast<long long>(a.max_pages) * a.page_tokens;
+
+  int t = max(t0, a.row_start[0]), b = -1;
+  int first = 0, last = 0, past = 0;  // rows [first, last) of sequence b
+  while (t < t_end) {
+    if (b < 0 || t >= last) {
+      b = find_sequence(a.row_start, a.B, t);
+      if (b < 0) return;  // rows outside every sequence are left alone
+      first = a.row_start[b];
+      last = min(a.row_start[b + 1], a.T);
+      past = a.past_len[b];
+      if (past < 0 || first < 0 || last <= t ||
+          static_cast<long long>(past) + (last - first) > capacity) {
+        if (lane == 0) raise_cache_error();
+        if (last <= t) return;
+        t = last;  // the sequence does not fit its table: none of it is written
+        continue;
+      }
+    }
+    const int pos = past + (t - first);
+    const int in_block = pos % kBlockTokens;
+    const int stop = min(t + kBlockTokens - in_block, last);
+    if (in_block != 0 && t != first) {  // a block that an earlier row began
+      t = stop;
+      continue;
+    }
+    const int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
+    if (page < 0 || page >= a.pages) {
+      if (lane == 0) raise_cache_error();
+      t = stop;
+      continue;
+    }
+    const int slot = pos % a.page_tokens - in_block;  // the block's first slot
+    const long long hp = static_cast<long long>(page) * a.heads + head;
+    int8_t* blk = codes + (hp * a.page_tokens + slot) * D;
+    float* sp = scales + hp * (a.page_tokens / kBlockTokens) + slot / kBlockTokens;
+    const int count = stop - t;
+
+    uint4 raw[CPL];
+    float amax = 0.0f;
+    const float s_old = in_block ? *sp : 0.0f;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = lane + 32 * i, tok = c / TC, ch = c % TC;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (tok < count)
+        raw[i] = __ldcs(reinterpret_cast<const uint4*>(x + (t + tok) * stride + head * D + 8 * ch));
+    }
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
+    }
+    amax = warp_max(amax);
+    const float s = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
+    const float r = __frcp_rn(s);
+    const bool fast = s > 0.0f && r <= 3.0e38f;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = lane + 32 * i, tok = c / TC, ch = c % TC;
+      if (tok >= count) continue;
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      float v[8];
+      uint32_t q[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = bf16lo(w[e]);
+        v[2 * e + 1] = bf16hi(w[e]);
+      }
+      if (fast) {
+        quantize8_recip<127>(v, s, r, q);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = static_cast<uint32_t>(quantize<127>(v[e], s));
+      }
+      *reinterpret_cast<uint2*>(blk + (in_block + tok) * D + 8 * ch) =
+          make_uint2(pack_low_bytes(q[0], q[1], q[2], q[3]), pack_low_bytes(q[4], q[5], q[6], q[7]));
+    }
+    __syncwarp();  // every lane has read the old scale
+    if (s > s_old && in_block) {  // the older tokens take the new scale
+      const float ratio = __fdiv_rn(s_old, s);
+      for (int c = lane; c < in_block * (D / 4); c += 32) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(blk) + c;
+        const uint32_t w = *p;
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float old = static_cast<float>(static_cast<int8_t>(w >> (8 * e)));
+          q[e] = static_cast<uint32_t>(__float2int_rn(__fmul_rn(old, ratio)));
+        }
+        *p = pack_low_bytes(q[0], q[1], q[2], q[3]);
+      }
+    }
+    if (lane == 0 && (!in_block || s > s_old)) *sp = s;
+    t = stop;
+  }
+}
+
+// ------------------------------------------------------------ attention
+
+// D (16 x 8, fp32) += A (16 x 16, f16) x B (16 x 8, f16).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two bytes (code + 128) that `sel` picks out of w, as two f16 codes, exactly: placed
+// under the exponent of 1024 (f16 holds integers up to 2048), then 1152 taken off.
+__device__ __forceinline__ uint32_t bytes_f16x2(uint32_t w, uint32_t sel) {
+  const uint32_t u = __byte_perm(w, 0x64646464u, sel);
+  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(1152.0f, 1152.0f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 16-byte chunk `chunk` of row `row` in a tile of D-byte rows as the copy engine's
+// 128-byte (D = 128) or 64-byte (D = 64) swizzle leaves it.
+template <int D>
+__device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
+  return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4)
+                  : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+}
+
+constexpr int kAttnWarps = 4;
+constexpr int kAttnCtasPerSm = 2;
+constexpr int kAttnMinUnits = 16;  // blocks of 16 tokens a CTA takes at least
+
+// Softmax weights enter the second product in f16 as 2^kPShift times their value
+// relative to a reference maximum that the running one may exceed by up to 2^kPSlack
+// before the sums are rescaled: at most 2^15 (f16 reaches 65504), full 11 bits down to
+// 2^-25 of the reference.
+constexpr float kPShift = 11.0f, kPSlack = 4.0f;
+
+struct AttnArgs {
+  const uint16_t* q;      // bf16 rows [Tq], heads x D packed within a row
+  long long q_stride;     // elements between rows
+  const int* q_start;     // [B + 1]
+  const int* kv_len;      // [B]
+  const int* table;       // [B][max_pages]
+  const float* k_scale;   // [pages][kv_heads][page_tokens / 16]
+  const float* v_scale;
+  uint16_t* out;          // bf16 [Tq][q_heads][D]
+  float* lse;             // [Tq][q_heads] or null
+  long long* prefix;      // workspace: [B + 1] units before each sequence
+  float* partial;         // workspace: [grid][2] partial results
+  int Tq, B, q_heads, kv_heads, max_pages, pages, page_tokens, causal;
+  float scale_log2;       // softmax scale * log2(e)
+};
+
+// What a sequence asks for: the work is cut into units of one block of 16 tokens for one
+// item, an item being one cache head and one tile of query rows.  An item without any
+// block counts one unit, so that its rows are written.
+struct SeqWork {
+  int q0, nq, len;       // query rows [q0, q0 + nq), cached tokens
+  int tiles;             // row tiles per cache head
+  int blocks;            // units per item
+  long long units;
+};
+
+template <int RT>
+__device__ __forceinline__ SeqWork sequence_work(const AttnArgs& a, int b, bool report) {
+  SeqWork w;
+  const long long capacity = static_cast<long long>(a.max_pages) * a.page_tokens;
+  const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
+  w.q0 = min(max(s0, 0), a.Tq);
+  w.nq = max(min(s1, a.Tq) - w.q0, 0);
+  const int len = a.kv_len[b];
+  w.len = static_cast<int>(min(static_cast<long long>(max(len, 0)), capacity));
+  if (report && (len < 0 || len > capacity || s0 < 0 || s1 > a.Tq || s1 < s0)) raise_cache_error();
+  const int G = a.q_heads / a.kv_heads;
+  w.tiles = static_cast<int>((static_cast<long long>(w.nq) * G + RT - 1) / RT);
+  w.blocks = max(1, (w.len + kBlockTokens - 1) / kBlockTokens);
+  w.units = static_cast<long long>(w.tiles) * w.blocks * a.kv_heads;
+  return w;
+}
+
+__device__ __forceinline__ long long units_per_cta(long long total, int grid) {
+  return max(static_cast<long long>(kAttnMinUnits), (total + grid - 1) / grid);
+}
+
+// One CTA of four warps takes an equal share of all units (so ragged batches stay
+// balanced and one long sequence fills the GPU), item by item.  WR warps cover the rows
+// of a tile (16 each), the other factor 4 / WR of the warps take the blocks in turn.
+// Each such token group has its own ring of STAGES blocks (16 x D keys and values), filled
+// by bulk tensor copies that its first warp issues, so the warps run independently
+// between the ends of items.  Codes become f16 in registers, exactly; q enters as f16
+// after a power-of-two scaling per row that keeps all its 8 bits; scores, maxima, sums
+// and the output are fp32.  Block scales multiply the scores (keys) and the softmax
+// weights relative to a power-of-two reference (values).
+template <int D, int WR>
+struct AttnCfg {
+  static constexpr int WT = kAttnWarps / WR;   // token groups
+  static constexpr int RT = 16 * WR;           // rows per tile
+  static constexpr int TILE = kBlockTokens * D;
+  static constexpr int STAGES = 65536 / (WT * 2 * TILE) < 8 ? 65536 / (WT * 2 * TILE) : 8;
+  static constexpr int RING = WT * STAGES * 2 * TILE;
+  static constexpr int SLAB_STRIDE = D + 4;
+  static constexpr int SLABS = kAttnWarps * 16 * SLAB_STRIDE * 4;
+  static constexpr int SMEM = RING + SLABS + 1024;  // + alignment
+  static constexpr int PARTIAL = RT * (D + 2);      // floats of one partial result
+};
+
+template <int D, int WR>
+__global__ void __launch_bounds__(32 * kAttnWarps, kAttnCtasPerSm) attn_kv8_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const AttnArgs a) {
+  using C = AttnCfg<D, WR>;
+  constexpr int WT = C::WT, RT = C::RT, STAGES = C::STAGES, TILE = C::TILE;
+  constexpr int KS = D / 16;   // matrix steps over the channels
+  constexpr int ND = D / 8;    // 8-channel tiles of the output
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* slabs = reinterpret_cast<float*>(ring + C::RING);
+  __shared__ __align__(8) uint64_t full[WT][STAGES], empty[WT][STAGES];
+  __shared__ float row_m[kAttnWarps][16], row_l[kAttnWarps][16];
+  __shared__ long long scan[kAttnWarps + 1];
+  __shared__ long long start_rem;
+  __shared__ int start_b;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wt = warp / WR, wr = warp % WR;
+  const int G = a.q_heads / a.kv_heads;
+  uint8_t* my_ring = ring + wt * STAGES * 2 * TILE;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < WT; ++i)
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_init(&full[i][s], 1);
+        mbar_init(&empty[i][s], WR);
+      }
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    start_b = -1;
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // Units before every sequence: each thread sums a run of them, then a scan over threads.
+  const int per_thread = (a.B + 32 * kAttnWarps - 1) / (32 * kAttnWarps);
+  const int b_lo = min(static_cast<int>(threadIdx.x) * per_thread, a.B);
+  const int b_hi = min(b_lo + per_thread, a.B);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += sequence_work<RT>(a, b, blockIdx.x == 0).units;
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xFFFFFFFFu, before, o);
+    if (lane >= o) before += up;
+  }
+  if (lane == 31) scan[warp] = before;
+  __syncthreads();
+  before -= mine;
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  const long long per = units_per_cta(total, gridDim.x);
+  const long long u_begin = min(per * blockIdx.x, total), u_end = min(u_begin + per, total);
+  if (blockIdx.x == 0 || (u_begin >= before && u_begin < before + mine)) {
+    long long at = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long n = sequence_work<RT>(a, b, false).units;
+      if (blockIdx.x == 0) a.prefix[b] = at;
+      if (u_begin >= at && u_begin < at + n) {
+        start_b = b;
+        start_rem = u_begin - at;
+      }
+      at += n;
+    }
+    if (blockIdx.x == 0 && b_hi == a.B && b_lo < b_hi) a.prefix[a.B] = at;
+  }
+  __syncthreads();
+  if (u_begin >= u_end) return;
+
+  int b = start_b;
+  long long rem = start_rem;
+  uint32_t phase = 0;  // blocks this token group has taken so far (stage and parity)
+  SeqWork sw = sequence_work<RT>(a, b, false);
+  for (long long u = u_begin; u < u_end;) {
+    while (rem >= sw.units) {  // the next sequence that has any work
+      rem = 0;
+      sw = sequence_work<RT>(a, ++b, false);
+    }
+    const long long item = rem / sw.blocks;
+    const int j0 = static_cast<int>(rem % sw.blocks);
+    const int take = static_cast<int>(min(static_cast<long long>(sw.blocks - j0), u_end - u));
+    const int head = static_cast<int>(item / sw.tiles), tile = static_cast<int>(item % sw.tiles);
+    const int rows = sw.nq * G;
+    const int r_first = tile * RT, r_last = min(r_first + RT, rows) - 1;
+    // tokens that the tile's last row sees, which no earlier row exceeds
+    const int reach = a.causal ? max(0, sw.len - sw.nq + r_last / G + 1) : sw.len;
+    const int j1 = min(j0 + take, (reach + kBlockTokens - 1) / kBlockTokens);
+    const int count = j1 - j0 > wt ? (j1 - j0 - wt + WT - 1) / WT : 0;  // my blocks
+
+    // my rows: g and g + 8 of the warp's sixteen
+    int see[2];
+    const uint16_t* qp[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r_first + 16 * wr + 8 * h + g;
+      const bool valid = r < rows;
+      const int qi = valid ? r / G : 0, qh = head * G + (valid ? r % G : 0);
+      see[h] = valid && a.causal ? sw.len - sw.nq + qi + 1 : sw.len;
+      qp[h] = valid ? a.q + (sw.q0 + qi) * a.q_stride + static_cast<long long>(qh) * D : nullptr;
+    }
+    int see_min = min(see[0], see[1]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) see_min = min(see_min, __shfl_xor_sync(0xFFFFFFFFu, see_min, o));
+
+    // upcoming blocks of this group, one per lane: row of the copy, scales
+    const long long cap_blocks = a.page_tokens / kBlockTokens;
+    auto look_up = [&](int group, int& copy_row, float& sk, float& sv) {
+      const int i = 32 * group + lane;
+      copy_row = 0;
+      sk = sv = 0.0f;
+      if (i >= count) return;
+      const int pos = (j0 + wt + WT * i) * kBlockTokens;
+      int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
+      if (page < 0 || page >= a.pages) {
+        raise_cache_error();
+        page = 0;
+      }
+      const long long hp = static_cast<long long>(page) * a.kv_heads + head;
+      const int slot = pos % a.page_tokens;
+      copy_row = static_cast<int>(hp * a.page_tokens + slot);
+      sk = a.k_scale[hp * cap_blocks + slot / kBlockTokens];
+      sv = a.v_scale[hp * cap_blocks + slot / kBlockTokens];
+    };
+    int row_a, row_b;
+    float sk_a, sv_a, sk_b, sv_b;
+    look_up(0, row_a, sk_a, sv_a);
+    look_up(1, row_b, sk_b, sv_b);
+
+    auto issue = [&](int i, int consumed) {  // copies of my block i
+      const bool cur = (i >> 5) == (consumed >> 5);
+      const int copy_row = __shfl_sync(0xFFFFFFFFu, cur ? row_a : row_b, i & 31);
+      if (wr == 0) {
+        const uint32_t n = phase + i, st = n % STAGES, round = n / STAGES;
+        bool ok = true;
+        if (WR > 1 && round > 0) ok = mbar_wait_drain(&empty[wt][st], (round - 1) & 1);
+        if (lane == 0 && ok) {
+          mbar_arrive_expect_tx(&full[wt][st], 2 * TILE);
+          tma_load_2d(my_ring + st * 2 * TILE, &tm_k, &full[wt][st], 0, copy_row);
+          tma_load_2d(my_ring + st * 2 * TILE + TILE, &tm_v, &full[wt][st], 0, copy_row);
+        }
+      }
+      __syncwarp();
+    };
+    const int ahead = min(count, STAGES);
+    for (int i = 0; i < ahead; ++i) issue(i, 0);
+
+    // q of my rows as f16 operands; channel 32t' + 16s + 4w + 0..3 (D = 128; 16t + 4w for
+    // D = 64) of a row is what lane t's word w of its load s holds of a key
+    uint32_t qf[KS][4];
+    float qs[2];  // undoes the rows' power-of-two scaling, times the softmax scale
+    {
+      uint4 raw[2][D / 32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          raw[h][i] = qp[h] ? *reinterpret_cast<const uint4*>(qp[h] + t * (D / 4) + 8 * i)
+                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = fmaxf(top, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // the largest value of the row comes to lie in [2^14, 2^15)
+        const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
+        const float up = __uint_as_float((268u - e) << 23);
+        qs[h] = __uint_as_float((e - 14u) << 23) * a.scale_log2;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+#pragma unroll
+          for (int e2 = 0; e2 < 4; ++e2)
+            qf[2 * i + (e2 >> 1)][h + 2 * (e2 & 1)] =
+                pack_half2(bf16lo(w[e2]) * up, bf16hi(w[e2]) * up);
+        }
+      }
+    }
+
+    float o[ND][4] = {};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float ref = 0.0f, inv_ref = 0.0f;  // power of two >= the value scales seen
+    int dead = -1;  // the block whose copy did not arrive in time
+    int issued = ahead;
+    // a stage is refilled when its readers are done: at once where there is one reader,
+    // one block later where several warps share it, so that none waits for the slowest
+    constexpr int LAG = WR > 1 ? 1 : 0;
+    for (int i = 0; i < count; ++i) {
+      const uint32_t n = phase + i, st = n % STAGES;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_drain(&full[wt][st], (n / STAGES) & 1))) {
+        dead = i;
+        break;
+      }
+      const uint8_t* kt = my_ring + st * 2 * TILE;
+      const uint8_t* vt = kt + TILE;
+      const float sk = __shfl_sync(0xFFFFFFFFu, sk_a, i & 31);
+      const float sv = __shfl_sync(0xFFFFFFFFu, sv_a, i & 31);
+
+      // scores of 16 tokens: columns of the two tiles are tokens 0-7 and 8-15
+      float s[2][4] = {};
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const int chunk = D == 128 ? 2 * t + c : t;
+          const uint4 kv = *reinterpret_cast<const uint4*>(kt + tile_offset<D>(8 * nt + g, chunk));
+          const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t u = w[e] ^ 0x80808080u;
+            const uint32_t (&f)[4] = qf[4 * c + e];
+            mma_f16(s[nt], f[0], f[1], f[2], f[3], bytes_f16x2(u, 0x4140), bytes_f16x2(u, 0x4342));
+          }
+        }
+      // values: lane (g, t) takes 16 (8) channels of tokens 2t, 2t+1, 2t+8, 2t+9
+      uint32_t vw[4][D / 32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
+        if constexpr (D == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(vt + tile_offset<D>(tok, g));
+          vw[k][0] = v.x; vw[k][1] = v.y; vw[k][2] = v.z; vw[k][3] = v.w;
+        } else {
+          const uint2 v =
+              *reinterpret_cast<const uint2*>(vt + tile_offset<D>(tok, g >> 1) + 8 * (g & 1));
+          vw[k][0] = v.x; vw[k][1] = v.y;
+        }
+      }
+      // the stage is in registers: refill it
+      __syncwarp();
+      if (WR > 1 && lane == 0) mbar_arrive(&empty[wt][st]);
+      if (issued < count && issued < i + 1 + STAGES - LAG) {
+        issue(issued, i);
+        ++issued;
+      }
+
+      const int first = (j0 + wt + WT * i) * kBlockTokens;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] *= qs[e >> 1] * sk;
+      if (first + kBlockTokens > see_min) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (first + 8 * nt + 2 * t + (e & 1) >= see[e >> 1]) s[nt][e] = -INFINITY;
+      }
+      float top[2];
+      bool grow = sv > ref;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 2));
+        grow |= top[h] > m[h] + kPSlack;
+      }
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        float shrink = 1.0f;
+        if (sv > ref) {
+          const uint32_t e = min((__float_as_uint(sv) >> 23) + 1u, 252u);
+          const float to = __uint_as_float(max(e, 2u) << 23);
+          inv_ref = __uint_as_float((254u - max(e, 2u)) << 23);
+          shrink = ref * inv_ref;
+          ref = to;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float f = 1.0f;
+          if (top[h] > m[h] + kPSlack) {
+            f = exp2_approx(m[h] - top[h]);  // 0 for the first maximum
+            m[h] = top[h];
+          }
+          l[h] *= f;
+          f *= shrink;
+#pragma unroll
+          for (int nd = 0; nd < ND; ++nd) {
+            o[nd][2 * h] *= f;
+            o[nd][2 * h + 1] *= f;
+          }
+        }
+      }
+      const float wv = sv * inv_ref;
+      uint32_t pf[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float base = m[h] == -INFINITY ? 0.0f : m[h] - kPShift;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float p0 = exp2_approx(s[nt][2 * h] - base);
+          const float p1 = exp2_approx(s[nt][2 * h + 1] - base);
+          l[h] += p0 + p1;
+          pf[nt][h] = pack_half2(p0 * wv, p1 * wv);
+        }
+      }
+      // o += p v: 4 x 4 bytes (four tokens, four channels) give four tiles' operands
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = vw[k][w] ^ 0x80808080u;
+        const uint32_t lo0 = __byte_perm(u[0], u[1], 0x5140), hi0 = __byte_perm(u[0], u[1], 0x7362);
+        const uint32_t lo1 = __byte_perm(u[2], u[3], 0x5140), hi1 = __byte_perm(u[2], u[3], 0x7362);
+        mma_f16(o[4 * w], pf[0][0], pf[0][1], pf[1][0], pf[1][1], bytes_f16x2(lo0, 0x4140),
+                bytes_f16x2(lo1, 0x4140));
+        mma_f16(o[4 * w + 1], pf[0][0], pf[0][1], pf[1][0], pf[1][1], bytes_f16x2(lo0, 0x4342),
+                bytes_f16x2(lo1, 0x4342));
+        mma_f16(o[4 * w + 2], pf[0][0], pf[0][1], pf[1][0], pf[1][1], bytes_f16x2(hi0, 0x4140),
+                bytes_f16x2(hi1, 0x4140));
+        mma_f16(o[4 * w + 3], pf[0][0], pf[0][1], pf[1][0], pf[1][1], bytes_f16x2(hi0, 0x4342),
+                bytes_f16x2(hi1, 0x4342));
+      }
+      if ((i & 31) == 31) {
+        row_a = row_b; sk_a = sk_b; sv_a = sv_b;
+        look_up((i >> 5) + 2, row_b, sk_b, sv_b);
+      }
+    }
+    if (dead >= 0 && wr == 0 && lane == 0)  // wait (bounded) for the copies in flight
+      for (int i = dead; i < issued; ++i)
+        mbar_wait_drain(&full[wt][(phase + i) % STAGES], ((phase + i) / STAGES) & 1);
+    phase += count;
+
+    // join the token groups: sums relative to the largest maximum, in group order
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
+      if (t == 0) {
+        row_m[warp][8 * h + g] = m[h];
+        row_l[warp][8 * h + g] = l[h];
+      }
+    }
+    __syncthreads();
+    float* slab = slabs + warp * 16 * C::SLAB_STRIDE;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < WT; ++i) top = fmaxf(top, row_m[i * WR + wr][8 * h + g]);
+      const float f = m[h] == -INFINITY ? 0.0f : exp2_approx(m[h] - top) * ref;
+      float* dst = slab + (8 * h + g) * C::SLAB_STRIDE + t * (D / 4);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int nd = 0; nd < ND; nd += 4)
+          *reinterpret_cast<float4*>(dst + part * ND + nd) =
+              make_float4(o[nd][2 * h + part] * f, o[nd + 1][2 * h + part] * f,
+                          o[nd + 2][2 * h + part] * f, o[nd + 3][2 * h + part] * f);
+    }
+    __syncthreads();
+    const bool whole = j0 == 0 && take == sw.blocks;
+    float* dst = a.partial + (static_cast<long long>(blockIdx.x) * 2 + (j0 > 0 ? 0 : 1)) * C::PARTIAL;
+    for (int i = threadIdx.x; i < RT * (D / 4); i += 32 * kAttnWarps) {
+      const int r = i / (D / 4), d = 4 * (i % (D / 4)), rw = r / 16, ri = r % 16;
+      if (r_first + r >= rows) break;
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k * WR + rw][ri]);
+      float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < WT; ++k) {
+        const float mk = row_m[k * WR + rw][ri];
+        if (mk != -INFINITY) sum += row_l[k * WR + rw][ri] * exp2_approx(mk - top);
+        const float4 p = *reinterpret_cast<const float4*>(
+            slabs + ((k * WR + rw) * 16 + ri) * C::SLAB_STRIDE + d);
+        v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+      }
+      if (whole) {
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const int qi = (r_first + r) / G, qh = head * G + (r_first + r) % G;
+        const long long at = static_cast<long long>(sw.q0 + qi) * a.q_heads + qh;
+        const __nv_bfloat162 x0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        const __nv_bfloat162 x1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(a.out + at * D + d) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
+        if (a.lse && d == 0)
+          a.lse[at] = sum > 0.0f ? (top - kPShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      } else {
+        *reinterpret_cast<float4*>(dst + r * D + d) = v;
+        if (d == 0) {
+          dst[RT * D + 2 * r] = top;
+          dst[RT * D + 2 * r + 1] = sum;
+        }
+      }
+    }
+    if (__syncthreads_or(dead >= 0)) return;  // the error word is set
+    u += take;
+    rem += take;
+  }
+}
+
+// Joins the partial results of items that several CTAs shared, in CTA order; a CTA per
+// query row and head, which returns at once where one CTA had the whole item.
+template <int D>
+__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, int grid, int RT) {
+  __shared__ float part[4][D + 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x / a.q_heads, qh = blockIdx.x % a.q_heads;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = find_sequence(a.q_start, a.B, row);
+  if (b < 0) return;
+  const int G = a.q_heads / a.kv_heads;
+  const int q0 = min(max(a.q_start[b], 0), a.Tq), nq = max(min(a.q_start[b + 1], a.Tq) - q0, 0);
+  if (row < q0 || row >= q0 + nq) return;
+  const long long units = a.prefix[b + 1] - a.prefix[b], total = a.prefix[a.B];
+  const int tiles = static_cast<int>((static_cast<long long>(nq) * G + RT - 1) / RT);
+  const long long blocks = units / (static_cast<long long>(tiles) * a.kv_heads);
+  const int r = (row - q0) * G + qh % G;
+  const long long u0 = a.prefix[b] + (static_cast<long long>(qh / G) * tiles + r / RT) * blocks;
+  const long long per = units_per_cta(total, grid);
+  const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + blocks - 1) / per);
+  if (c0 == c1) return;
+  const int ri = r % RT;
+  const long long size = static_cast<long long>(RT) * (D + 2);
+  auto slot = [&](int c) {
+    return a.partial + (2LL * c + (static_cast<long long>(c) * per > u0 ? 0 : 1)) * size;
+  };
+
+  float top = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, slot(c)[RT * D + 2 * ri]);
+  top = warp_max(top);
+  float acc[D / 32] = {}, sum = 0.0f;
+  if (top != -INFINITY) {
+#pragma unroll 4
+    for (int c = c0 + warp; c <= c1; c += 4) {
+      const float* p = slot(c);
+      const float f = exp2_approx(p[RT * D + 2 * ri] - top);  // 0 for an empty part
+      sum += p[RT * D + 2 * ri + 1] * f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] += p[ri * D + lane * (D / 32) + e] * f;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) part[warp][lane * (D / 32) + e] = acc[e];
+  if (lane == 0) part[warp][D] = sum;
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= D) return;
+  const float all = part[0][D] + part[1][D] + part[2][D] + part[3][D];
+  const float v = part[0][d] + part[1][d] + part[2][d] + part[3][d];
+  const long long at = static_cast<long long>(row) * a.q_heads + qh;
+  a.out[at * D + d] =
+      __bfloat16_as_ushort(__float2bfloat16_rn(all > 0.0f ? v / all : 0.0f));
+  if (a.lse && d == 0)
+    a.lse[at] = all > 0.0f ? (top - kPShift + log2f(all)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ------------------------------------------------------------ host side
+
+// Row-warps of a tile: as many as the average sequence's rows per cache head need, up to
+// four (a tile of 64 rows reads each block once for all of them).
+int attn_row_warps(int Tq, int B, int q_heads, int kv_heads) {
+  const long long rows = static_cast<long long>(Tq) * (q_heads / kv_heads);
+  return rows <= 16LL * B ? 1 : rows <= 32LL * B ? 2 : 4;
+}
+
+size_t attn_prefix_bytes(int B) { return (8 * (static_cast<size_t>(B) + 1) + 255) / 256 * 256; }
+
+bool cache_map(CUtensorMap* m, const void* base, int D, long long rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(D), kBlockTokens};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int WR>
+cudaError_t run_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int grid,
+                     cudaStream_t st) {
+  using C = AttnCfg<D, WR>;
+  static std::atomic<bool> done[kAttrDevices];
+  const cudaError_t e = set_smem_once(attn_kv8_kernel<D, WR>, C::SMEM, done);
+  if (e != cudaSuccess) return e;
+  const cudaError_t f = launch_pdl(attn_kv8_kernel<D, WR>, grid, 32 * kAttnWarps, C::SMEM, st, 1,
+                                   tm_k, tm_v, a);
+  if (f != cudaSuccess) return f;
+  return launch_pdl(attn_kv8_join_kernel<D>, a.Tq * a.q_heads, 128, 0, st, 1, a, grid, C::RT);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const Kv8Append& p, cudaStream_t st) {
+  AppendArgs a;
+  a.x[0] = p.k; a.x[1] = p.v;
+  a.stride[0] = p.k_stride; a.stride[1] = p.v_stride;
+  a.row_start = p.row_start; a.past_len = p.past_len; a.table = p.cache.table;
+  a.codes[0] = p.cache.k_codes; a.codes[1] = p.cache.v_codes;
+  a.scale[0] = p.cache.k_scale; a.scale[1] = p.cache.v_scale;
+  a.T = p.T; a.B = p.cache.B; a.max_pages = p.cache.max_pages; a.pages = p.cache.pages;
+  a.heads = p.cache.kv_heads; a.page_tokens = p.cache.page_tokens;
+  a.window = p.T > 16LL * a.B ? 16 : 1;
+  const long long windows = (p.T + a.window - 1) / a.window;
+  const int grid = static_cast<int>((windows * a.heads * 2 + 3) / 4);
+  return p.cache.D == 128 ? launch_pdl(kv8_append_kernel<128>, grid, 128, 0, st, 1, a)
+                          : launch_pdl(kv8_append_kernel<64>, grid, 128, 0, st, 1, a);
+}
+
+size_t attn_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int D) {
+  const size_t rt = 16 * attn_row_warps(Tq, B, q_heads, kv_heads);
+  const size_t grid = static_cast<size_t>(sm_count()) * kAttnCtasPerSm;
+  return attn_prefix_bytes(B) + (grid * 2 * rt * (D + 2) * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_attn_kv8(const Kv8Attn& p, cudaStream_t st) {
+  const long long rows = static_cast<long long>(p.cache.pages) * p.cache.kv_heads * p.cache.page_tokens;
+  CUtensorMap tm_k, tm_v;
+  if (!cache_map(&tm_k, p.cache.k_codes, p.cache.D, rows) ||
+      !cache_map(&tm_v, p.cache.v_codes, p.cache.D, rows))
+    return cudaErrorInvalidValue;
+  AttnArgs a;
+  a.q = p.q; a.q_stride = p.q_stride; a.q_start = p.q_start; a.kv_len = p.kv_len;
+  a.table = p.cache.table; a.k_scale = p.cache.k_scale; a.v_scale = p.cache.v_scale;
+  a.out = p.out; a.lse = p.lse;
+  a.prefix = static_cast<long long*>(p.workspace);
+  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + attn_prefix_bytes(p.cache.B));
+  a.Tq = p.Tq; a.B = p.cache.B; a.q_heads = p.q_heads; a.kv_heads = p.cache.kv_heads;
+  a.max_pages = p.cache.max_pages; a.pages = p.cache.pages; a.page_tokens = p.cache.page_tokens;
+  a.causal = p.causal; a.scale_log2 = p.scale * 1.4426950408889634f;
+  const int grid = sm_count() * kAttnCtasPerSm;
+  const int wr = attn_row_warps(p.Tq, p.cache.B, p.q_heads, p.cache.kv_heads);
+#define WQ_ATTN(D_)                                                          \
+  return wr == 1   ? run_attn<D_, 1>(tm_k, tm_v, a, grid, st)                \
+         : wr == 2 ? run_attn<D_, 2>(tm_k, tm_v, a, grid, st)                \
+                   : run_attn<D_, 4>(tm_k, tm_v, a, grid, st)
+  if (p.cache.D == 128) WQ_ATTN(128);
+  WQ_ATTN(64);
+#undef WQ_ATTN
+}
+
+}  // namespace wq

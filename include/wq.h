@@ -75,13 +75,17 @@ typedef enum {
 /* Device error bits reported by wq_device_status(). */
 #define WQ_DEVICE_ERR_TIMEOUT 1u
 #define WQ_DEVICE_ERR_STREAM_ID 2u
+#define WQ_DEVICE_ERR_CACHE 4u /* wq_kv8_append / wq_attn_kv8: a page, length or row table entry \
+                                  outside its range */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* wq_status_string(wq_status s);
 
 /* ABI version of this library (major * 100 + minor; the minor number grows when
- * entry points are added, the major one when an existing signature or contract
- * changes).  101: adds wq_gemm_plan_query. */
+ * entry points of the fused linear are added, the major one when an existing
+ * signature or contract changes).  101: adds wq_gemm_plan_query.  The operators
+ * beside the linear (wq_pack_int4_group, wq_gemv_w4g, wq_kv8_append, wq_attn_kv8)
+ * leave it as it is; a caller that may meet an older library looks up the symbol. */
 int wq_version(void);
 
 /* Bytes of device workspace wq_linear_w4a8 / wq_linear_w4a4 need for M token
@@ -338,6 +342,107 @@ wq_status wq_linear_w4a8_noalloc(const wq_bf16* x, int M, int K, int N, const fl
                                  const float* beta, int S, int T, int step, const uint8_t* qw,
                                  const float* s_w, const float* bias, wq_bf16* y,
                                  wq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators beside the fused linear, for steps of one to a few tokens: a
+ * weight-only product whose int4 weights have a scale per group of channels, and
+ * attention over a paged int8 cache of the keys and values of earlier tokens.
+ * The conventions at the top of this file hold, except that scales, biases, tables
+ * of integers, lse and the product's y need only their element's alignment (other
+ * tensors 16 bytes, workspaces 256).
+ * --------------------------------------------------------------------------- */
+
+/* Offline weight preparation (Figure 2) with a scale per group of input channels:
+ * W' = fp32(W) * c (c may be NULL, meaning 1),
+ *   s_g[k/group][n] = bf16(max over the group of |W'[n,k]| / 7)
+ *   code[n,k]       = clamp(rint_half_even(W'[n,k] / s_g), -7, 7), 0 where s_g is 0
+ * with IEEE fp32 divisions; the codes are decided by the rounded scale.
+ *   W [N][K] bf16; group 32, 64 or 128 (else WQ_ERR_ARG); N >= 1;
+ *   qw [N][K/2] uint8 out; s_g [K/group][N] bf16 out.
+ * Layout of qw (not wq_pack_int4's): in each run of 128 channels (64 bytes, sixteen
+ * little-endian 32-bit words) word 4t + j, for t, j in 0..3, holds channels
+ * 32j + 8t .. 32j + 8t + 7 of the run; of these eight, channel 2i is nibble i and
+ * channel 2i + 1 nibble i + 4 (nibble 0 the lowest), two's complement. */
+wq_status wq_pack_int4_group(const wq_bf16* W, const float* c, int N, int K, int group,
+                             uint8_t* qw, wq_bf16* s_g, wq_stream_t stream);
+
+/* The weight-only linear for one to a few tokens, on wq_pack_int4_group's weights:
+ *   y[m,n] = bf16( sum_k x'[m,k] * s_g[k/group][n] * code[n,k] + bias[n] )
+ *   x'[m,k] = fp32(x[m,k]) * cinv[k] (cinv may be NULL, meaning 1)
+ * with fp32 sums.  Without cinv the products are exact; with it x' enters as the sum
+ * of two bf16 values, an error of at most 2^-17 of x'.
+ *   x [M][K] bf16, 0 <= M <= 16; bias [N] fp32 or NULL; y [M][N] bf16 out; any N >= 1.
+ * No workspace. */
+wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
+                      const uint8_t* qw, const wq_bf16* s_g, int group, const float* bias,
+                      wq_bf16* y, wq_stream_t stream);
+
+/* The cache.  `pages` pages of `page_tokens` (16, 32, 64 or 128) tokens each hold, per
+ * head of head_dim (64 or 128) channels, int8 codes and one fp32 scale per block of 16
+ * tokens, for keys and values each; a cached value is scale * code:
+ *   k_codes, v_codes [pages][kv_heads][page_tokens][head_dim] int8
+ *   k_scale, v_scale [pages][kv_heads][page_tokens / 16] fp32
+ * Token p of sequence b lies in page block_table[b][p / page_tokens], slot
+ * p % page_tokens; block_table [B][max_pages] int32, entries behind a sequence's last
+ * page are not read.  Allocating, sharing and freeing pages is the caller's: sequences
+ * may share pages that are only read, but a block that is appended to must be in one
+ * sequence's table only.  Limits: pages * kv_heads * page_tokens and max_pages *
+ * page_tokens below 2^31.
+ *
+ * Appends new tokens: row r of k and v (bf16, kv_heads * head_dim elements packed
+ * within a row, rows k_stride / v_stride elements apart, a multiple of 8) with
+ * row_start[b] <= r < row_start[b+1] becomes token past_len[b] + r - row_start[b] of
+ * sequence b.  row_start [B+1], past_len [B] int32; rows outside [row_start[0],
+ * row_start[B]) are not read.  For each block of 16 tokens with new ones, head, and
+ * keys or values:
+ *   s_new = max(s_old, max |x| / 127)    s_old: the block's scale if it holds tokens
+ *                                        before past_len[b], else 0
+ *   new code = clamp(rint_half_even(x / s_new), -127, 127), 0 where s_new is 0
+ *   old code = rint_half_even(old code * (s_old / s_new))   where s_new > s_old
+ * in IEEE fp32: the scale is that of the largest value in the block, however the tokens
+ * came; a token costs at most half a step when it is written and half a step each time
+ * a later token of its block raises the scale.  Slots behind the new tokens keep their
+ * contents.
+ * Checked on the device: 0 <= past_len, the tokens fit max_pages, the pages used are in
+ * [0, pages), row_start does not decrease and stays within [0, T].  A violation sets
+ * WQ_DEVICE_ERR_CACHE and writes nothing for that sequence (or page). */
+wq_status wq_kv8_append(const wq_bf16* k, const wq_bf16* v, int64_t k_stride, int64_t v_stride,
+                        int T, const int32_t* row_start, const int32_t* past_len, int B,
+                        const int32_t* block_table, int max_pages, int8_t* k_codes,
+                        int8_t* v_codes, float* k_scale, float* v_scale, int pages, int kv_heads,
+                        int page_tokens, int head_dim, wq_stream_t stream);
+
+/* Bytes of device workspace wq_attn_kv8 needs on the current device (partial results of
+ * the parts that several SMs share); 0 for invalid sizes. */
+size_t wq_attn_kv8_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int head_dim);
+
+/* Attention over the cache.  Row r of q (bf16, q_heads * head_dim packed within a row,
+ * rows q_stride elements apart, a multiple of 8), q_start[b] <= r < q_start[b+1], is
+ * query i = r - q_start[b] of sequence b, whose cache holds kv_len[b] tokens.  Query head
+ * h reads cache head h / (q_heads / kv_heads).
+ *   out[r][h] = bf16( sum_j p_j v_j / sum_j p_j ),  p_j = exp(scale * q . k_j)
+ * over all kv_len[b] tokens (causal == 0: the queries and the cached tokens may be
+ * sequences of different lengths), or, with causal != 0, over tokens
+ * j <= kv_len[b] - n + i, n the sequence's number of queries: the queries are its last n
+ * tokens.  A query that sees no token gets out = 0 and lse = -infinity.
+ *   q_start [B+1], kv_len [B] int32; out [Tq][q_heads][head_dim] bf16, rows outside every
+ *   sequence are left as they were; lse [Tq][q_heads] fp32 or NULL: log of the sum of
+ *   p_j, with which results over several caches can be joined.
+ * Scores, softmax and sums are fp32; q keeps all its bits, the softmax weights are
+ * rounded to 11 bits for the product with the codes.  For the same arguments the result
+ * is the same on every call; calls that may run at the same time need workspaces of
+ * their own.  Work is shared out from kv_len and q_start as they are on the device, so a
+ * captured call may be replayed after they changed.
+ * Checked on the device: kv_len in [0, max_pages * page_tokens], pages in [0, pages),
+ * q_start as row_start above.  A violation sets WQ_DEVICE_ERR_CACHE; lengths are then cut
+ * to their range and a bad page is read as page 0. */
+wq_status wq_attn_kv8(const wq_bf16* q, int64_t q_stride, int Tq, int q_heads,
+                      const int32_t* q_start, const int32_t* kv_len, int B,
+                      const int32_t* block_table, int max_pages, const int8_t* k_codes,
+                      const int8_t* v_codes, const float* k_scale, const float* v_scale,
+                      int pages, int kv_heads, int page_tokens, int head_dim, int causal,
+                      float scale, wq_bf16* out, float* lse, void* workspace, size_t ws_bytes,
+                      wq_stream_t stream);
 
 /* Reads and clears the device error word of the current device (synchronizes
  * the device).  *flags receives the WQ_DEVICE_ERR_* bits seen since the last
