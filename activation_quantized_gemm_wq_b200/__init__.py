@@ -170,9 +170,10 @@ def _codes_per_row(K, act_bits):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        import torch
+        # the raw handle alone: building a torch Stream object costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 

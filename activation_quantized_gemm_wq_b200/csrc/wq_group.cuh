@@ -14,6 +14,7 @@
 // pair of x as it lies in memory.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "wq_internal.h"
 #include "wq_ptx.cuh"
@@ -80,196 +81,593 @@ __global__ void __launch_bounds__(256) pack_int4_group_kernel(
 
 // ------------------------------------------------------------ matrix-vector products
 
-// D (16 x 8, fp32) += A (16 x 16, bf16) x B (16 x 8, bf16).
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D (16 x 8, int32) = (first ? 0 : D) + A (16 x 32, int8) x B (32 x 8, int8).
+__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                       uint32_t b1, bool first) {
+  if (first)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Nibble pair i of a packed word as two bf16 codes, exactly: code + 8 placed under the
-// exponent of 128 (bf16 holds integers up to 256), then 136 taken off.
+// D (16 x 8, fp32) += A (16 x 16, f16) x B (16 x 8, f16).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// (w & mask) ^ magic, one three-input operation.
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t u;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(u) : "r"(w), "r"(mask), "r"(magic));
+  return u;
+}
+
+// The nibble pairs 0 (I = 0) or 1 (I = 1) of w as two f16 codes, exactly: code + 8 placed
+// under the exponent of 1024 (f16 holds integers up to 2048), at bit 0 or bit 4, then 1032
+// taken off, or a sixteenth taken and 72 taken off.
 template <int I>
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w) {
-  const uint32_t u = ((w >> (4 * I)) & 0x000F000Fu) ^ 0x43084308u;
-  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                   __floats2bfloat162_rn(136.0f, 136.0f));
+__device__ __forceinline__ uint32_t codes_f16x2(uint32_t w) {
+  const uint32_t u = I == 0 ? and_xor(w, 0x000F000Fu, 0x64086408u) : and_xor(w, 0x00F000F0u, 0x64806480u);
+  const __half2 h = *reinterpret_cast<const __half2*>(&u);
+  const __half2 v = I == 0 ? __hsub2(h, __floats2half2_rn(1032.0f, 1032.0f))
+                           : __hfma2(h, __floats2half2_rn(0.0625f, 0.0625f),
+                                     __floats2half2_rn(-72.0f, -72.0f));
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// One byte of each of four words -> one word.
+__device__ __forceinline__ uint32_t gather_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                                 uint32_t byte) {
+  const uint32_t sel = byte | (byte + 4) << 4;
+  return __byte_perm(__byte_perm(a, b, sel), __byte_perm(c, d, sel), 0x5410);
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
   return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
 }
 
-// x' = x * cinv in two bf16 parts, hi + lo (16 bits of it: an error of at most 2^-17).
-__device__ __forceinline__ void fold_pair(uint32_t x, float c0, float c1, uint32_t& hi,
-                                          uint32_t& lo) {
-  const float a = __fmul_rn(bf16lo(x), c0), b = __fmul_rn(bf16hi(x), c1);
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  const __nv_bfloat162 l =
-      __floats2bfloat162_rn(__fsub_rn(a, __low2float(h)), __fsub_rn(b, __high2float(h)));
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+constexpr int kGemvWarps = 16;
+constexpr int kGemvMaxSplit = 8;            // CTAs that share K (a portable cluster)
+constexpr int kGemvMaxSmem = 226 * 1024;
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
 }
 
-constexpr int kGemvWarps = 8;
+// 3-D tiled load global -> shared, completion counted on an mbarrier.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* desc, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
 
-// CTA = 16 MT output channels; its warps take the runs of 128 input channels in turn, so
-// that the warps read neighbouring 64-byte pieces of each row at the same time.  Each
-// lane keeps PF runs of weights in flight in registers (16 bytes per row and run).  The
-// weights are the instruction's A operand (16 output channels x 16 input channels), the
-// tokens its 8 columns; sums within a group and across groups are fp32, and a group's
-// scale multiplies its fp32 sum.  The warps' sums meet in shared memory, in warp order.
-// FOLD: x' = x * cinv enters as two bf16 parts, two instructions instead of one.
-template <int G, int MT, int NT, int PF, bool FOLD>
-__global__ void __launch_bounds__(32 * kGemvWarps) gemv_w4g_kernel(
-    const uint16_t* __restrict__ x, const float* __restrict__ cinv,
-    const uint8_t* __restrict__ qw, const uint16_t* __restrict__ s_g,
-    const float* __restrict__ bias, uint16_t* __restrict__ y, int M, int K, int N) {
-  constexpr int R = 16 * MT, C = 8 * NT;
-  __shared__ float red[kGemvWarps][C][R + 1];
+struct GemvArgs {
+  const uint16_t* x;     // bf16 [M][K]
+  const float* cinv;     // [K] or null
+  const uint16_t* s_g;   // bf16 [K / G][N]
+  const float* bias;     // [N] or null
+  uint16_t* y;           // bf16 [M][N]
+  int M, K, N;
+  int S;                 // CTAs of a cluster, each with a share of K
+  int share;             // runs of 128 channels in a share (the last may have fewer)
+  int tiles;             // row tiles of a cluster (the last may have fewer)
+};
+
+// MT: 16-channel halves of a row tile; NT: groups of four tokens (1 or 2, digits; 4, f16);
+// TINY: one or two tokens, whose lowest digits fill the columns that hi and mid leave free.
+template <int MT, int NT, bool TINY>
+struct GemvCfg {
+  static constexpr int WR = 16 * MT;               // output channels of a row tile
+  static constexpr int RPS = MT == 1 ? 2 : 1;      // runs per stage (2 KB tiles)
+  static constexpr int STAGES = NT == 4 ? 2 : 3;
+  static constexpr int TILE = RPS * WR * 64;
+  static constexpr int RING = kGemvWarps * STAGES * TILE;
+  static constexpr bool HALF = NT == 4;            // tokens as f16 instead of digits
+  static constexpr int COLS = HALF ? 4 : TINY ? 1 : NT + 1;  // KB of staged tokens a run
+  static constexpr int TOKENS = TINY ? 2 : 4 * NT;
+  static constexpr int SEG = TOKENS * WR;             // floats of a segment's sums
+  static constexpr int run_bytes(int group) { return COLS * 1024 + 128 / group * TOKENS * 4; }
+  static constexpr int smem(int share, int group, int tiles) {
+    return RING + share * run_bytes(group) + (tiles + kGemvWarps - 1) * SEG * 4 + 128;
+  }
+};
+
+// Weight streaming is the bound, so copies in flight and few instructions per weight are
+// what counts.  One CTA per SM; a cluster of S CTAs makes `tiles` row tiles of 16 MT output
+// channels, each CTA from its share of K.  The CTA's work, row tile by row tile, is one
+// sequence of stages (a row tile x RPS runs of 128 input channels), of which each warp takes
+// an equal piece: it has a ring of its own that bulk tensor copies keep full across row
+// tiles, and waits for no other warp between its first and last stage.  What a warp sums
+// for one row tile is a segment; segments meet in shared memory when all is done, in warp
+// order, and the shares through the cluster's shared window, in rank order.
+//
+// The products run on the integer matrix instructions: a nibble moved to the high half of
+// its byte is 16 * code, so eight codes cost one shift and two masks, where making them
+// floating-point costs eleven instructions.  The tokens become 22-bit integers relative to
+// the largest |x'| of their group (a power-of-two scale: a value is off by at most 2^-22 of
+// that maximum, and bf16 values down to 2^-14 of it are exact), split into three signed
+// bytes, hi 2^16 + mid 2^8 + lo.  hi and mid of a token are neighbouring columns of one
+// column tile, so that a lane holds both sums; the lo of eight tokens fill another (TINY:
+// columns 4 and 6).  The sums of a group are exact in int32; they are joined, scaled and
+// added over the groups in fp32.
+//
+// Staged layout: column tile c, run r: 1 KB [half][column][t][16 bytes], the 16 bytes of
+// half h being the channels of words j = 2h, 2h + 1, in the order 0 4 1 5, 2 6 3 7 in
+// which the masks leave the codes.
+//
+// More than eight tokens (HALF) would need six column tiles and the joining of as many
+// sums, which takes longer than the copies; they enter as f16 instead, 11 bits of x' over
+// a power-of-two scale per group, against codes made f16 (exact; nine instructions for
+// eight codes), two column tiles of eight tokens.  Staged run: 2 KB per column tile,
+// [word j][column][t][8 channels].
+template <int G, int MT, int NT, bool TINY>
+__global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
+    const __grid_constant__ CUtensorMap tm_w, const GemvArgs a) {
+  using Cfg = GemvCfg<MT, NT, TINY>;
+  constexpr int WR = Cfg::WR, RPS = Cfg::RPS, STAGES = Cfg::STAGES, SEG = Cfg::SEG;
+  constexpr int COLS = Cfg::COLS, TOKENS = Cfg::TOKENS;
+  constexpr bool HALF = Cfg::HALF;
+  constexpr int THREADS = 32 * kGemvWarps;
+  extern __shared__ uint8_t gemv_smem[];
+  __shared__ __align__(8) uint64_t full[kGemvWarps][STAGES];
+  uint8_t* ring_all = gemv_smem + ((128u - (smem_u32(gemv_smem) & 127u)) & 127u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * R;
-  const int runs = K / 128;
-  const size_t row_bytes = static_cast<size_t>(K) / 2;
+  const int S = a.S, M = a.M, N = a.N;
+  const int rank = blockIdx.x % S, tile0 = blockIdx.x / S * a.tiles;
+  const int tiles = min(a.tiles, (N + WR - 1) / WR - tile0);
+  const int all = a.K / 128;
+  const int r_begin = min(rank * a.share, all), runs = min(a.share, all - r_begin);
+  const int per_tile = (runs + RPS - 1) / RPS;                         // stages
+  const int total = tiles * per_tile;
+  const int u_begin = static_cast<int>(static_cast<long long>(total) * warp / kGemvWarps);
+  const int u_end = static_cast<int>(static_cast<long long>(total) * (warp + 1) / kGemvWarps);
+  const int count = u_end - u_begin;
 
-  // rows past N repeat the last one: read in bounds, never written
-  const uint8_t* wp[MT][2];
-  int row[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      row[mt][h] = min(n0 + 16 * mt + 8 * h + g, N - 1);
-      wp[mt][h] = qw + row[mt][h] * row_bytes + 16 * t;
-    }
+  uint8_t* ring = ring_all + warp * STAGES * Cfg::TILE;
+  uint8_t* xs = ring_all + Cfg::RING;                                    // [share][COLS] KB
+  float* xscale = reinterpret_cast<float*>(xs + a.share * COLS * 1024);  // [group][TOKENS]
+  float* segs = xscale + a.share * (128 / G) * TOKENS;
+
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(&full[warp][s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   griddep_wait();
   griddep_launch_dependents();
 
-  uint4 w[PF][MT][2];
-  uint16_t s[PF][MT][2];
-  auto fetch = [&](int p, int run) {
-    const size_t gi = (static_cast<size_t>(run) * 128 + 32 * t) / G;  // lane t: the group of word t
+  // copies and scales run ahead of the sums: the row tile and the stage within it
+  int c_tile = count > 0 ? u_begin / per_tile : 0, c_k = u_begin - c_tile * per_tile;
+  int s_tile = c_tile, s_k = c_k;
+  const int first_tile = c_tile, first_k = c_k;
+  auto issue = [&](int i) {  // copies of my stage i
+    if (lane == 0) {
+      uint64_t* bar = &full[warp][i % STAGES];
+      mbar_arrive_expect_tx(bar, Cfg::TILE);
+      tma_load_3d(ring + i % STAGES * Cfg::TILE, &tm_w, bar, 0, (tile0 + c_tile) * WR,
+                  r_begin + c_k * RPS);
+    }
+    if (++c_k == per_tile) {
+      c_k = 0;
+      ++c_tile;
+    }
+  };
+  for (int i = 0; i < STAGES && i < count; ++i) issue(i);
+
+  // scales two stages ahead in registers; lane t: the group of word t
+  uint16_t sc[2][RPS][MT][2];
+  const uint16_t* s_base = a.s_g + static_cast<size_t>(r_begin * 128 + 32 * t) / G * N;
+  const size_t run_step = static_cast<size_t>(128 / G) * N;
+  const uint16_t* sp[MT][2];
+  auto scale_rows = [&]() {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        w[p][mt][h] = __ldcs(reinterpret_cast<const uint4*>(wp[mt][h] + static_cast<size_t>(run) * 64));
-        s[p][mt][h] = __ldg(s_g + gi * N + row[mt][h]);
-      }
+      for (int h = 0; h < 2; ++h)
+        sp[mt][h] = s_base + s_k * RPS * run_step +
+                    min((tile0 + s_tile) * WR + 16 * mt + 8 * h + g, N - 1);
   };
+  auto load_scales = [&](uint16_t (&to)[RPS][MT][2]) {
 #pragma unroll
-  for (int p = 0; p < PF; ++p) {
-    const int run = warp + p * kGemvWarps;
-    if (run < runs) fetch(p, run);
+    for (int rr = 0; rr < RPS; ++rr)
+      if (s_k * RPS + rr < runs)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            to[rr][mt][h] = __ldg(sp[mt][h]);
+            sp[mt][h] += run_step;
+          }
+    if (++s_k == per_tile) {
+      s_k = 0;
+      ++s_tile;
+      scale_rows();
+    }
+  };
+  if (count > 0) {
+    scale_rows();
+    load_scales(sc[0]);
+    if (count > 1) load_scales(sc[1]);
   }
 
-  float acc[MT][NT][4] = {};
-  for (int base = warp; base < runs; base += PF * kGemvWarps) {
+  // The tokens of this share: a thread takes eight channels, XB times at a time (the loads
+  // of a batch are in flight together); the G / 8 threads of a group are neighbours and
+  // share its maximum by shuffles.  Tokens past M become zeros.
+  {
+    constexpr int XB = 4;
+    const int pieces = runs * 16, pieces_all = TOKENS * pieces;
+    const uint32_t inv = pieces > 1 ? 0xFFFFFFFFu / pieces + 1 : 0;  // at / pieces, at < 2^18
+    for (int base = threadIdx.x; base - static_cast<int>(threadIdx.x) < pieces_all;
+         base += XB * THREADS) {
+      uint4 raw[XB];
 #pragma unroll
-    for (int p = 0; p < PF; ++p) {
-      const int run = base + p * kGemvWarps;
-      if (run < runs) {
-        float sum[MT][NT][4] = {};
+      for (int e = 0; e < XB; ++e) {
+        const int at = base + e * THREADS, m = __umulhi(at, inv), pc = at - m * pieces;
+        raw[e] = make_uint4(0, 0, 0, 0);
+        if (at < pieces_all && m < M)
+          raw[e] = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(m) * a.K) +
+                         r_begin * 16 + pc);
+      }
+#pragma unroll
+      for (int e = 0; e < XB; ++e) {
+        if (base - static_cast<int>(threadIdx.x) + e * THREADS >= pieces_all) break;  // uniform
+        const int at = base + e * THREADS, m = __umulhi(at, inv), pc = at - m * pieces;
+        const bool valid = at < pieces_all;
+        float ci[8], v[8];
+        load_cinv8_global(valid ? a.cinv : nullptr, r_begin * 16 + pc, ci);
+        scale8(raw[e], ci, v);
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(v[c]));
+#pragma unroll
+        for (int o = G / 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        // digits: 2^(21 - E) with 2^E <= top < 2^(E + 1); f16: 2^(14 - E); at most 2^127
+        constexpr uint32_t BITS = HALF ? 14 : 21;
+        const uint32_t ex = max(__float_as_uint(top) >> 23, BITS);
+        const float up = __uint_as_float((254u + BITS - ex) << 23);
+        if (!valid) continue;
+        const int run = pc >> 4, j = (pc >> 2) & 3, tt = pc & 3, nt = m >> 2;
+        uint8_t* dst = xs + run * (COLS * 1024);
+        if constexpr (HALF) {
+          *reinterpret_cast<uint4*>(dst + (m >> 3) * 2048 + j * 512 + (m & 7) * 64 + tt * 16) =
+              make_uint4(pack_half2(v[0] * up, v[1] * up), pack_half2(v[2] * up, v[3] * up),
+                         pack_half2(v[4] * up, v[5] * up), pack_half2(v[6] * up, v[7] * up));
+        } else {
+          uint32_t d[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)  // rounded to an integer in the low bits, as signed bytes
+            d[c] = (__float_as_uint(__fadd_rn(__fmul_rn(v[c], up), kRoundMagic)) -
+                    (0x4B400000u - 0x00808080u)) ^ 0x00808080u;
+          dst += (j >> 1) * 512 + tt * 16 + (j & 1) * 8;
+#pragma unroll
+          for (int b = 0; b < 3; ++b) {
+            const int tile = TINY ? 0 : b == 0 ? NT : nt;
+            const int col = 2 * (m & 3) + (b > 0 ? 2 - b : TINY ? 4 : nt & 1);
+            *reinterpret_cast<uint2*>(dst + tile * 1024 + col * 64) =
+                make_uint2(gather_bytes(d[0], d[4], d[1], d[5], b),
+                           gather_bytes(d[2], d[6], d[3], d[7], b));
+          }
+        }
+        // 2^(E - BITS), and the digits' 1 / 16 of the codes
+        if (pc % (G / 8) == 0)
+          xscale[pc / (G / 8) * TOKENS + m] =
+              __uint_as_float((ex - BITS + 1u) << 23) * (HALF ? 0.5f : 0.03125f);
+      }
+    }
+  }
+  __syncthreads();
+
+  // acc[mt][i][h]: row 16 mt + 8 h + g; token 4 i + t, or (HALF) 8 (i / 2) + 2 t + i % 2
+  float acc[MT][NT][2] = {};
+  bool dead = false;
+  int k = first_k, tile_now = first_tile;
+  auto take = [&](uint16_t (&scale)[RPS][MT][2], int i) {
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait_drain(&full[warp][i % STAGES], (i / STAGES) & 1))) {
+      dead = true;
+      return;
+    }
+    const uint8_t* tile = ring + i % STAGES * Cfg::TILE + g * 64 + 16 * t;
+#pragma unroll
+    for (int rr = 0; rr < RPS; ++rr) {
+      const int run = k * RPS + rr;
+      if (rr > 0 && run >= runs) break;
+      const uint8_t* xp = xs + run * (COLS * 1024) + g * 64 + t * 16;
+      const float* xf = xscale + run * (128 / G * TOKENS) + (HALF ? 2 * t : TINY ? t & 1 : t);
+      uint4 w[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[mt][h] = *reinterpret_cast<const uint4*>(tile + (rr * WR + 16 * mt + 8 * h) * 64);
+      auto row_scale = [&](int mt, int h, int j) {
+        const uint32_t v = static_cast<uint32_t>(scale[rr][mt][h]) << 16;
+        return __uint_as_float(G == 128 ? v : __shfl_sync(0xFFFFFFFFu, v, (lane & 28) | j));
+      };
+      if constexpr (HALF) {
+        float sum[MT][2][4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int k = run * 128 + 32 * j + 8 * t;
-          uint32_t b[NT][4], bl[NT][4];
+          uint4 b[2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int m = 8 * nt + g;
-            uint4 xv = make_uint4(0, 0, 0, 0);
-            if (m < M) xv = __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K + k));
-            b[nt][0] = xv.x; b[nt][1] = xv.y; b[nt][2] = xv.z; b[nt][3] = xv.w;
-          }
-          if constexpr (FOLD) {
-            float ci[8];
-            load_cinv8_global(cinv, k / 8, ci);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                fold_pair(b[nt][e], ci[2 * e], ci[2 * e + 1], b[nt][e], bl[nt][e]);
-          }
+          for (int c = 0; c < 2; ++c)
+            b[c] = *reinterpret_cast<const uint4*>(xp + c * 2048 + j * 512);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const uint32_t wa = word_of(w[p][mt][0], j), wb = word_of(w[p][mt][1], j);
-            const uint32_t a0[4] = {codes_bf16x2<0>(wa), codes_bf16x2<0>(wb),
-                                    codes_bf16x2<1>(wa), codes_bf16x2<1>(wb)};
-            const uint32_t a1[4] = {codes_bf16x2<2>(wa), codes_bf16x2<2>(wb),
-                                    codes_bf16x2<3>(wa), codes_bf16x2<3>(wb)};
+            const uint32_t wa = word_of(w[mt][0], j), wb = word_of(w[mt][1], j);
+            const uint32_t va = wa >> 8, vb = wb >> 8;
+            const uint32_t f[8] = {codes_f16x2<0>(wa), codes_f16x2<0>(wb), codes_f16x2<1>(wa),
+                                   codes_f16x2<1>(wb), codes_f16x2<0>(va), codes_f16x2<0>(vb),
+                                   codes_f16x2<1>(va), codes_f16x2<1>(vb)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(sum[mt][nt], a0, b[nt][0], b[nt][1]);
-              mma_bf16(sum[mt][nt], a1, b[nt][2], b[nt][3]);
-              if constexpr (FOLD) {
-                mma_bf16(sum[mt][nt], a0, bl[nt][0], bl[nt][1]);
-                mma_bf16(sum[mt][nt], a1, bl[nt][2], bl[nt][3]);
-              }
+            for (int c = 0; c < 2; ++c) {
+              mma_f16(sum[mt][c], f[0], f[1], f[2], f[3], b[c].x, b[c].y);
+              mma_f16(sum[mt][c], f[4], f[5], f[6], f[7], b[c].z, b[c].w);
             }
           }
-          if ((j + 1) % (G / 32) == 0) {  // the group ends: scale its sum
+          if ((j + 1) % (G / 32) == 0) {  // the group ends
+            float2 fx[2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              float sc[2];
+            for (int c = 0; c < 2; ++c)
+              fx[c] = *reinterpret_cast<const float2*>(xf + j / (G / 32) * TOKENS + 8 * c);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t v = static_cast<uint32_t>(s[p][mt][h]) << 16;
-                sc[h] = __uint_as_float(
-                    G == 128 ? v : __shfl_sync(0xFFFFFFFFu, v, (lane & 28) | j));
+                const float fw = row_scale(mt, h, j);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {  // (fw * fx may underflow)
+                  float* q = &sum[mt][c][2 * h];
+                  acc[mt][2 * c][h] = fmaf(q[0] * fx[c].x, fw, acc[mt][2 * c][h]);
+                  acc[mt][2 * c + 1][h] = fmaf(q[1] * fx[c].y, fw, acc[mt][2 * c + 1][h]);
+                  q[0] = q[1] = 0.0f;
+                }
               }
+          }
+        }
+      } else {
+        int sum[MT][COLS][4];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+        for (int half = 0; half < 2; ++half) {
+          uint4 b[COLS];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  acc[mt][nt][e] = fmaf(sum[mt][nt][e], sc[e >> 1], acc[mt][nt][e]);
-                  sum[mt][nt][e] = 0.0f;
+          for (int c = 0; c < COLS; ++c)
+            b[c] = *reinterpret_cast<const uint4*>(xp + c * 1024 + half * 512);
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int j = 2 * half + jj;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const uint32_t wa = word_of(w[mt][0], j), wb = word_of(w[mt][1], j);
+              const uint32_t f[4] = {(wa << 4) & 0xF0F0F0F0u, (wb << 4) & 0xF0F0F0F0u,
+                                     wa & 0xF0F0F0F0u, wb & 0xF0F0F0F0u};
+#pragma unroll
+              for (int c = 0; c < COLS; ++c)
+                mma_s8(sum[mt][c], f, jj ? b[c].z : b[c].x, jj ? b[c].w : b[c].y,
+                       j % (G / 32) == 0);
+            }
+            if ((j + 1) % (G / 32) == 0) {  // the group ends
+              float fx[NT];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) fx[nt] = xf[j / (G / 32) * TOKENS + 4 * nt];
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float fw = row_scale(mt, h, j);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    const int* hm = sum[mt][nt] + 2 * h;
+                    const int low = TINY ? __shfl_xor_sync(0xFFFFFFFFu, hm[0], 2)
+                                         : sum[mt][COLS - 1][2 * h + (nt & 1)];
+                    const float v24 = fmaf(static_cast<float>(hm[0]), 65536.0f,
+                                           static_cast<float>(hm[1] * 256 + low));
+                    // (fw * fx may underflow)
+                    acc[mt][nt][h] = fmaf(v24 * fx[nt], fw, acc[mt][nt][h]);
+                  }
                 }
             }
           }
         }
-        const int next = run + PF * kGemvWarps;
-        if (next < runs) fetch(p, next);
       }
     }
+    __syncwarp();  // the stage has been read
+    if (i + STAGES < count) issue(i + STAGES);
+    if (i + 2 < count) load_scales(scale);
+    if (++k == per_tile || i + 1 == count) {  // the segment ends
+      float* seg = segs + (tile_now + warp) * SEG;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int m = HALF ? 8 * (nt >> 1) + 2 * t + (nt & 1) : 4 * nt + t;
+            if (!TINY || t < 2) seg[m * WR + 16 * mt + 8 * h + g] = acc[mt][nt][h];
+            acc[mt][nt][h] = 0.0f;
+          }
+      k = 0;
+      ++tile_now;
+    }
+  };
+  int i = 0;
+  for (; i < count && !dead; i += 2) {
+    take(sc[0], i);
+    if (i + 1 < count && !dead) take(sc[1], i + 1);
   }
-
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        red[warp][8 * nt + 2 * t + (e & 1)][16 * mt + 8 * (e >> 1) + g] = acc[mt][nt][e];
+  if (dead && lane == 0)  // a copy did not arrive in time: wait (bounded) for all of them
+    for (int q = max(0, i - 2); q < min(count, i + STAGES); ++q)
+      mbar_wait_drain(&full[warp][q % STAGES], (q / STAGES) & 1);
   __syncthreads();
-  for (int i = threadIdx.x; i < R * M; i += 32 * kGemvWarps) {
-    const int r = i % R, m = i / R, n = n0 + r;
-    if (n >= N) continue;
-    float v = bias ? bias[n] : 0.0f;
-    float sum = 0.0f;
-#pragma unroll
-    for (int q = 0; q < kGemvWarps; ++q) sum += red[q][m][r];
-    y[static_cast<size_t>(m) * N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum + v));
+
+  // Row tile q's segments are those of the warps whose pieces overlap [q, q + 1) per_tile;
+  // segment (tile, warp) lies at tile + warp.
+  auto tile_sum = [&](int q, int at) {
+    const int lo = (kGemvWarps * q * per_tile + kGemvWarps - 1) / total;
+    const int hi = (kGemvWarps * (q + 1) * per_tile - 1) / total;
+    float v = 0.0f;
+    for (int w = lo; w <= hi; ++w)
+      if (total * w / kGemvWarps < total * (w + 1) / kGemvWarps) v += segs[(q + w) * SEG + at];
+    return v;
+  };
+  float* part = reinterpret_cast<float*>(ring_all);  // [tile][token][channel]
+  if (S > 1) {
+    for (int q = threadIdx.x; q < tiles * SEG; q += THREADS)
+      part[q] = total > 0 ? tile_sum(q / SEG, q % SEG) : 0.0f;
+    cluster_sync();
   }
+  for (int q = threadIdx.x + rank * THREADS; q < tiles * SEG; q += THREADS * S) {
+    const int m = q % SEG / WR, n = (tile0 + q / SEG) * WR + q % WR;
+    if (m >= M || n >= N) continue;
+    float v = 0.0f;
+    if (S > 1) {
+      float p[kGemvMaxSplit];
+#pragma unroll
+      for (int c = 0; c < kGemvMaxSplit; ++c) p[c] = c < S ? ld_cluster_f32(mapa_shared(part + q, c)) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < kGemvMaxSplit; ++c) v += p[c];
+    } else {
+      v = tile_sum(q / SEG, q % SEG);
+    }
+    a.y[static_cast<size_t>(m) * N + n] =
+        __bfloat16_as_ushort(__float2bfloat16_rn(v + (a.bias ? a.bias[n] : 0.0f)));
+  }
+  if (S > 1) cluster_sync();  // nobody leaves while its sums are read
 }
 
-template <int G, int MT, int NT, int PF, bool FOLD>
+bool group_map(CUtensorMap* m, const void* base, int K, int N, int rows, int runs_per_box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(K / 128)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K / 2), 64};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(runs_per_box)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Row tiles a cluster may take at most: their joined sums lie over the ring, and their
+// segments beside the staged tokens.
+template <int G, int MT, int NT, bool TINY>
+constexpr int gemv_tiles_limit(int share) {
+  using Cfg = GemvCfg<MT, NT, TINY>;
+  const int by_ring = Cfg::RING / (Cfg::SEG * 4);
+  const int by_smem = (kGemvMaxSmem - Cfg::smem(share, G, 0)) / (Cfg::SEG * 4);
+  return by_ring < by_smem ? by_ring : by_smem;
+}
+
+// Clusters of S CTAs, one CTA per SM, that run at the same time on the current device (a
+// GPU's SMs come in groups that larger clusters do not fill: 148, 74, 33 and 15 clusters
+// of 1, 2, 4 and 8 here).  Asked once per device.
+template <class Kernel>
+int gemv_clusters(Kernel kernel, int S) {
+  static std::atomic<int> known[kAttrDevices][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  const int at = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3;
+  const bool cached = dev >= 0 && dev < kAttrDevices;
+  int n = cached ? known[dev][at].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  cudaLaunchConfig_t q = {};
+  q.gridDim = dim3(S);
+  q.blockDim = dim3(32 * kGemvWarps);
+  q.dynamicSmemBytes = kGemvMaxSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  q.attrs = attr;
+  q.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &q) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = sm_count() / S > 0 ? sm_count() / S : 1;
+  }
+  if (cached) known[dev][at].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int G, int MT, int NT, bool TINY>
 cudaError_t run_gemv(const uint16_t* x, const float* cinv, const uint8_t* qw, const uint16_t* s_g,
                      const float* bias, uint16_t* y, int M, int K, int N, cudaStream_t st) {
-  const int grid = (N + 16 * MT - 1) / (16 * MT);
-  return launch_pdl(gemv_w4g_kernel<G, MT, NT, PF, FOLD>, grid, 32 * kGemvWarps, 0, st, 1, x, cinv,
-                    qw, s_g, bias, y, M, K, N);
+  using Cfg = GemvCfg<MT, NT, TINY>;
+  const int runs = K / 128, tiles = (N + Cfg::WR - 1) / Cfg::WR;
+  static std::atomic<bool> done[kAttrDevices];
+  const cudaError_t e = set_smem_once(gemv_w4g_kernel<G, MT, NT, TINY>, kGemvMaxSmem, done);
+  if (e != cudaSuccess) return e;
+  // The split of K, by what an SM has to do, in KB of weights: the tiles of its clusters,
+  // staging its share of the tokens (each takes about as long as a quarter of a KB per
+  // run), and the exchange of the sums (about 1 us) where there is one.
+  int S = 0, per_cluster = 0;
+  long long best = 0;
+  for (int c = 1; c <= kGemvMaxSplit && c <= runs; c *= 2) {
+    const int share = (runs + c - 1) / c;
+    const int limit = gemv_tiles_limit<G, MT, NT, TINY>(share);
+    if (limit < 1) continue;
+    const int clusters = gemv_clusters(gemv_w4g_kernel<G, MT, NT, TINY>, c);
+    int take = (tiles + clusters - 1) / clusters;
+    if (take > limit) take = limit;
+    const long long waves = ((tiles + take - 1) / take + clusters - 1) / clusters;
+    const long long cost = waves * (4LL * take * share * MT + Cfg::TOKENS * share + (c > 1 ? 184 : 0));
+    if (S == 0 || cost < best) {
+      best = cost;
+      S = c;
+      per_cluster = take;
+    }
+  }
+  if (S == 0) return cudaErrorInvalidValue;
+  const int share = (runs + S - 1) / S;
+  CUtensorMap tm;
+  if (!group_map(&tm, qw, K, N, Cfg::WR, Cfg::RPS)) return cudaErrorInvalidValue;
+  const GemvArgs a{x, cinv, s_g, bias, y, M, K, N, S, share, per_cluster};
+  const int grid = (tiles + per_cluster - 1) / per_cluster * S;
+  return launch_pdl(gemv_w4g_kernel<G, MT, NT, TINY>, grid, 32 * kGemvWarps,
+                    Cfg::smem(share, G, per_cluster), st, S, tm, a);
 }
 
-template <int G, bool FOLD>
+template <int G>
 cudaError_t dispatch_gemv(const uint16_t* x, const float* cinv, const uint8_t* qw,
                           const uint16_t* s_g, const float* bias, uint16_t* y, int M, int K, int N,
                           cudaStream_t st) {
-  if (M <= 8) return run_gemv<G, 1, 1, 4, FOLD>(x, cinv, qw, s_g, bias, y, M, K, N, st);
-  return run_gemv<G, 1, 2, 4, FOLD>(x, cinv, qw, s_g, bias, y, M, K, N, st);
+  // the largest split must hold the staged tokens; where it cannot (more than 8 tokens of
+  // long rows), 8 tokens at a time
+  const int share = (K / 128 + kGemvMaxSplit - 1) / kGemvMaxSplit;
+  const int most = M > 8 && gemv_tiles_limit<G, 2, 4, false>(share) < 4 ? 8 : M;
+  for (int m = 0; m < M; m += most) {
+    const int n = M - m < most ? M - m : most;
+    const uint16_t* xm = x + static_cast<size_t>(m) * K;
+    uint16_t* ym = y + static_cast<size_t>(m) * N;
+    const cudaError_t e =
+        n <= 2   ? run_gemv<G, 1, 1, true>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
+        : n <= 4 ? run_gemv<G, 2, 1, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
+        : n <= 8 ? run_gemv<G, 2, 2, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
+                 : run_gemv<G, 2, 4, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -288,9 +686,7 @@ cudaError_t launch_pack_int4_group(const uint16_t* W, const float* c, int N, int
 cudaError_t launch_gemv_w4g(const uint16_t* x, const float* cinv, const uint8_t* qw,
                             const uint16_t* s_g, int group, const float* bias, uint16_t* y, int M,
                             int K, int N, cudaStream_t st) {
-#define WQ_GEMV(G_)                                                                       \
-  return cinv ? dispatch_gemv<G_, true>(x, cinv, qw, s_g, bias, y, M, K, N, st)           \
-              : dispatch_gemv<G_, false>(x, cinv, qw, s_g, bias, y, M, K, N, st)
+#define WQ_GEMV(G_) return dispatch_gemv<G_>(x, cinv, qw, s_g, bias, y, M, K, N, st)
   if (group == 32) WQ_GEMV(32);
   if (group == 64) WQ_GEMV(64);
   WQ_GEMV(128);

@@ -10,6 +10,7 @@
 #pragma once
 #include <cuda_fp16.h>
 
+#include "wq_group.cuh"
 #include "wq_internal.h"
 #include "wq_ptx.cuh"
 #include "wq_quant.cuh"
@@ -191,16 +192,6 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const AppendArgs a) {
 
 // ------------------------------------------------------------ attention
 
-// D (16 x 8, fp32) += A (16 x 16, f16) x B (16 x 8, f16).
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -213,11 +204,6 @@ __device__ __forceinline__ uint32_t bytes_f16x2(uint32_t w, uint32_t sel) {
   const uint32_t u = __byte_perm(w, 0x64646464u, sel);
   const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(1152.0f, 1152.0f));
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // 16-byte chunk `chunk` of row `row` in a tile of D-byte rows as the copy engine's

@@ -369,8 +369,10 @@ wq_status wq_pack_int4_group(const wq_bf16* W, const float* c, int N, int K, int
 /* The weight-only linear for one to a few tokens, on wq_pack_int4_group's weights:
  *   y[m,n] = bf16( sum_k x'[m,k] * s_g[k/group][n] * code[n,k] + bias[n] )
  *   x'[m,k] = fp32(x[m,k]) * cinv[k] (cinv may be NULL, meaning 1)
- * with fp32 sums.  Without cinv the products are exact; with it x' enters as the sum
- * of two bf16 values, an error of at most 2^-17 of x'.
+ * with fp32 sums over the groups.  Up to 8 tokens x' is held in 22 bits below the
+ * largest |x'| of its group (off by at most 2^-22 of that, or 2^-128) and a group's sum is
+ * exact; beyond 8 tokens x' is rounded to 11 bits (bf16 values themselves are exact) and
+ * a group's sum is fp32.
  *   x [M][K] bf16, 0 <= M <= 16; bias [N] fp32 or NULL; y [M][N] bf16 out; any N >= 1.
  * No workspace. */
 wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,

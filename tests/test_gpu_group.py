@@ -82,9 +82,11 @@ def gemv(x, cinv, qw, s_g, group, bias):
 
 def check_gemv(x, cinv, qw, s_g, group, bias, y):
     """y against 64-bit sums.  One rounding to bf16 (half a step: 2^-8 relative, and the
-    subnormals' 2^-134) and fp32 sums: at most 16 matrix steps to a group's sum, K / 128
-    groups to a warp's, 16 warps and the bias, every addition within 2^-22 of the sum of
-    magnitudes (the matrix unit may truncate); with cinv another 2^-16 for x' in two parts."""
+    subnormals' 2^-134); fp32 sums over the K / group groups and at most 8 parts, with four
+    operations to a group's term, each within 2^-24 of the sum of magnitudes; and, up to
+    eight tokens, x' held to 2^-22 of its group's largest (or 2^-128), summed exactly; beyond
+    eight, x' in f16 (2^-11 relative, exact for bf16 itself; 2^-39 of the group's largest
+    where that is subnormal) and at most 8 matrix steps to a group's sum, each within 2^-22."""
     x8 = x.double()
     if cinv is not None:
         x8 = x8 * cinv.double()
@@ -95,9 +97,13 @@ def check_gemv(x, cinv, qw, s_g, group, bias, y):
     if bias is not None:
         ref, size = ref + bias.double(), size + bias.double().abs()
     K = x.shape[1]
-    steps = 16 + K / 128 + 16 + 1
-    allow = ref.abs() * 2.0 ** -8 + size * (steps * 2.0 ** -22 + (2.0 ** -16 if cinv is not None
-                                                                 else 0)) + 2.0 ** -133
+    top = x8.abs().view(-1, K // group, group).amax(-1).repeat_interleave(group, 1)
+    few = x.shape[0] <= 8
+    held = (top * 2.0 ** (-22 if few else -39) + 2.0 ** -128) @ w.abs().t()
+    steps = (K / group + 8 + 4) * 2.0 ** -24
+    if not few:
+        steps += 8 * 2.0 ** -22 + (2.0 ** -11 if cinv is not None else 0)
+    allow = ref.abs() * 2.0 ** -8 + size * steps + held + 2.0 ** -133
     bad = ~((y.double() - ref).abs() <= allow)
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outputs outside the bound"
 
