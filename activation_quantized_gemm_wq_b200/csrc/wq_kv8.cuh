@@ -215,7 +215,6 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
 }
 
 constexpr int kAttnWarps = 4;
-constexpr int kAttnCtasPerSm = 2;
 constexpr int kAttnMinUnits = 16;  // blocks of 16 tokens a CTA takes at least
 
 // Softmax weights enter the second product in f16 as 2^kPShift times their value
@@ -271,6 +270,114 @@ __device__ __forceinline__ long long units_per_cta(long long total, int grid) {
   return max(static_cast<long long>(kAttnMinUnits), (total + grid - 1) / grid);
 }
 
+// Units before every sequence: each thread sums a run of them, then a scan over threads.
+// Every CTA finds its share [begin, end) of them and where that starts: sequence b, unit
+// rem of it; CTA 0 leaves the sums for the joining kernel.
+struct AttnSched {
+  long long scan[kAttnWarps];
+  long long rem;
+  int b;
+};
+
+struct AttnShare {
+  long long begin, end, rem;
+  int b;
+};
+
+template <int RT>
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, AttnSched& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_thread = (a.B + 32 * kAttnWarps - 1) / (32 * kAttnWarps);
+  const int b_lo = min(static_cast<int>(threadIdx.x) * per_thread, a.B);
+  const int b_hi = min(b_lo + per_thread, a.B);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += sequence_work<RT>(a, b, blockIdx.x == 0).units;
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xFFFFFFFFu, before, o);
+    if (lane >= o) before += up;
+  }
+  if (lane == 31) sh.scan[warp] = before;
+  __syncthreads();
+  before -= mine;
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) {
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
+  }
+  AttnShare s;
+  const long long per = units_per_cta(total, gridDim.x);
+  s.begin = min(per * blockIdx.x, total);
+  s.end = min(s.begin + per, total);
+  if (blockIdx.x == 0 || (s.begin >= before && s.begin < before + mine)) {
+    long long at = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long n = sequence_work<RT>(a, b, false).units;
+      if (blockIdx.x == 0) a.prefix[b] = at;
+      if (s.begin >= at && s.begin < at + n) {
+        sh.b = b;
+        sh.rem = s.begin - at;
+      }
+      at += n;
+    }
+    if (blockIdx.x == 0 && b_hi == a.B && b_lo < b_hi) a.prefix[a.B] = at;
+  }
+  __syncthreads();
+  s.b = sh.b;
+  s.rem = sh.rem;
+  return s;
+}
+
+// The end of a segment: the token groups' sums are joined relative to the largest maximum,
+// in group order, and written as the result, or as a partial one where other CTAs have a
+// part of the item.  In shared memory: row_m, row_l [warp][ROWS] maxima and sums of the
+// warps' rows, slabs [warp][ROWS][D + 4] their outputs, already relative to that maximum.
+template <int D, int WR, int ROWS>
+__device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw,
+                                            const float (*row_m)[ROWS], const float (*row_l)[ROWS],
+                                            const float* slabs, int r_first, int head, bool whole,
+                                            bool from_start) {
+  constexpr int WT = kAttnWarps / WR, RT = ROWS * WR;
+  const int G = a.q_heads / a.kv_heads, rows = sw.nq * G;
+  float* dst = a.partial + (static_cast<long long>(blockIdx.x) * 2 + (from_start ? 1 : 0)) *
+                               (RT * (D + 2));
+  for (int i = threadIdx.x; i < RT * (D / 4); i += 32 * kAttnWarps) {
+    const int r = i / (D / 4), d = 4 * (i % (D / 4)), rw = r / ROWS, ri = r % ROWS;
+    if (r_first + r >= rows) break;
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k * WR + rw][ri]);
+    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < WT; ++k) {
+      const float mk = row_m[k * WR + rw][ri];
+      if (mk != -INFINITY) sum += row_l[k * WR + rw][ri] * exp2_approx(mk - top);
+      const float4 p = *reinterpret_cast<const float4*>(
+          slabs + ((k * WR + rw) * ROWS + ri) * (D + 4) + d);
+      v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+    }
+    if (whole) {
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const int qi = (r_first + r) / G, qh = head * G + (r_first + r) % G;
+      const long long at = static_cast<long long>(sw.q0 + qi) * a.q_heads + qh;
+      const __nv_bfloat162 x0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+      const __nv_bfloat162 x1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2*>(a.out + at * D + d) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
+      if (a.lse && d == 0)
+        a.lse[at] = sum > 0.0f ? (top - kPShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    } else {
+      *reinterpret_cast<float4*>(dst + r * D + d) = v;
+      if (d == 0) {
+        dst[RT * D + 2 * r] = top;
+        dst[RT * D + 2 * r + 1] = sum;
+      }
+    }
+  }
+}
+
 // One CTA of four warps takes an equal share of all units (so ragged batches stay
 // balanced and one long sequence fills the GPU), item by item.  WR warps cover the rows
 // of a tile (16 each), the other factor 4 / WR of the warps take the blocks in turn.
@@ -290,11 +397,11 @@ struct AttnCfg {
   static constexpr int SLAB_STRIDE = D + 4;
   static constexpr int SLABS = kAttnWarps * 16 * SLAB_STRIDE * 4;
   static constexpr int SMEM = RING + SLABS + 1024;  // + alignment
-  static constexpr int PARTIAL = RT * (D + 2);      // floats of one partial result
+  static constexpr int CTAS = D == 128 ? 2 : 3;     // per SM
 };
 
 template <int D, int WR>
-__global__ void __launch_bounds__(32 * kAttnWarps, kAttnCtasPerSm) attn_kv8_kernel(
+__global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, WR>::CTAS) attn_kv8_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const AttnArgs a) {
   using C = AttnCfg<D, WR>;
@@ -306,9 +413,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kAttnCtasPerSm) attn_kv8_kern
   float* slabs = reinterpret_cast<float*>(ring + C::RING);
   __shared__ __align__(8) uint64_t full[WT][STAGES], empty[WT][STAGES];
   __shared__ float row_m[kAttnWarps][16], row_l[kAttnWarps][16];
-  __shared__ long long scan[kAttnWarps + 1];
-  __shared__ long long start_rem;
-  __shared__ int start_b;
+  __shared__ AttnSched sched;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wt = warp / WR, wr = warp % WR;
@@ -324,52 +429,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kAttnCtasPerSm) attn_kv8_kern
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-    start_b = -1;
   }
   griddep_wait();
   griddep_launch_dependents();
 
-  // Units before every sequence: each thread sums a run of them, then a scan over threads.
-  const int per_thread = (a.B + 32 * kAttnWarps - 1) / (32 * kAttnWarps);
-  const int b_lo = min(static_cast<int>(threadIdx.x) * per_thread, a.B);
-  const int b_hi = min(b_lo + per_thread, a.B);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += sequence_work<RT>(a, b, blockIdx.x == 0).units;
-  long long before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xFFFFFFFFu, before, o);
-    if (lane >= o) before += up;
-  }
-  if (lane == 31) scan[warp] = before;
-  __syncthreads();
-  before -= mine;
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const long long per = units_per_cta(total, gridDim.x);
-  const long long u_begin = min(per * blockIdx.x, total), u_end = min(u_begin + per, total);
-  if (blockIdx.x == 0 || (u_begin >= before && u_begin < before + mine)) {
-    long long at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const long long n = sequence_work<RT>(a, b, false).units;
-      if (blockIdx.x == 0) a.prefix[b] = at;
-      if (u_begin >= at && u_begin < at + n) {
-        start_b = b;
-        start_rem = u_begin - at;
-      }
-      at += n;
-    }
-    if (blockIdx.x == 0 && b_hi == a.B && b_lo < b_hi) a.prefix[a.B] = at;
-  }
-  __syncthreads();
-  if (u_begin >= u_end) return;
+  const AttnShare share = attn_share<RT>(a, sched);
+  if (share.begin >= share.end) return;
 
-  int b = start_b;
-  long long rem = start_rem;
+  int b = share.b;
+  long long rem = share.rem;
+  const long long u_begin = share.begin, u_end = share.end;
   uint32_t phase = 0;  // blocks this token group has taken so far (stage and parity)
   SeqWork sw = sequence_work<RT>(a, b, false);
   for (long long u = u_begin; u < u_end;) {
@@ -655,41 +724,333 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kAttnCtasPerSm) attn_kv8_kern
                           o[nd + 2][2 * h + part] * f, o[nd + 3][2 * h + part] * f);
     }
     __syncthreads();
-    const bool whole = j0 == 0 && take == sw.blocks;
-    float* dst = a.partial + (static_cast<long long>(blockIdx.x) * 2 + (j0 > 0 ? 0 : 1)) * C::PARTIAL;
-    for (int i = threadIdx.x; i < RT * (D / 4); i += 32 * kAttnWarps) {
-      const int r = i / (D / 4), d = 4 * (i % (D / 4)), rw = r / 16, ri = r % 16;
-      if (r_first + r >= rows) break;
-      float top = -INFINITY, sum = 0.0f;
+    attn_finish<D, WR, 16>(a, sw, row_m, row_l, slabs, r_first, head,
+                           j0 == 0 && take == sw.blocks, j0 == 0);
+    if (__syncthreads_or(dead >= 0)) return;  // the error word is set
+    u += take;
+    rem += take;
+  }
+}
+
+// Tiles of at most eight query rows (decoding with up to eight query heads to a cache
+// head): the same work in fewer instructions, which is what bounds it.
+// Scores come from the integer matrix instructions, with the cached codes as they are: q
+// becomes 22-bit integers relative to its row's largest value (off by at most 2^-22 of
+// it), three signed bytes hi, mid, lo; rows 0 to 7 of one operand are hi, 8 to 15 mid, so
+// that a lane holds both sums, and a second operand has lo.  Sums over the channels are
+// exact.  A lane then holds the scores of row g for tokens 2t, 2t + 1, which is the layout
+// that the transposed product o^T += v^T p^T wants of p^T: half the instructions and
+// accumulators of o += p v, of whose sixteen rows eight would be empty.
+// A step is two blocks (32 tokens): the maxima, the reference and the barrier are looked
+// at once for both.
+template <int D>
+struct AttnFewCfg {
+  static constexpr int RT = 8, WT = kAttnWarps, TILE = kBlockTokens * D;
+  static constexpr int STEP = 4 * TILE;               // two blocks of keys and values
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int RING = WT * STAGES * STEP;
+  static constexpr int SLABS = kAttnWarps * RT * (D + 4) * 4;
+  static constexpr int SMEM = RING + 1024;            // + alignment; the slabs lie over the ring
+  static constexpr int CTAS = 3;
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D>::CTAS) attn_kv8_few_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const AttnArgs a) {
+  using C = AttnFewCfg<D>;
+  constexpr int WT = C::WT, RT = C::RT, STAGES = C::STAGES, TILE = C::TILE, STEP = C::STEP;
+  constexpr int KS = D / 32;   // matrix steps over the channels
+  constexpr int MD = D / 16;   // 16-channel tiles of the transposed output
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* slabs = reinterpret_cast<float*>(ring);
+  __shared__ __align__(8) uint64_t full[WT][STAGES];
+  __shared__ float row_m[kAttnWarps][RT], row_l[kAttnWarps][RT];
+  __shared__ AttnSched sched;
+
+  const int wt = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int G = a.q_heads / a.kv_heads;
+  uint8_t* my_ring = ring + wt * STAGES * STEP;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < WT; ++i)
+      for (int s = 0; s < STAGES; ++s) mbar_init(&full[i][s], 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const AttnShare share = attn_share<RT>(a, sched);
+  if (share.begin >= share.end) return;
+
+  int b = share.b;
+  long long rem = share.rem;
+  uint32_t phase = 0;  // steps this warp has taken so far (stage and parity)
+  SeqWork sw = sequence_work<RT>(a, b, false);
+  for (long long u = share.begin; u < share.end;) {
+    while (rem >= sw.units) {  // the next sequence that has any work
+      rem = 0;
+      sw = sequence_work<RT>(a, ++b, false);
+    }
+    const long long item = rem / sw.blocks;
+    const int j0 = static_cast<int>(rem % sw.blocks);
+    const int take = static_cast<int>(min(static_cast<long long>(sw.blocks - j0), share.end - u));
+    const int head = static_cast<int>(item / sw.tiles), tile = static_cast<int>(item % sw.tiles);
+    const int rows = sw.nq * G;
+    const int r_first = tile * RT, r_last = min(r_first + RT, rows) - 1;
+    const int reach = a.causal ? max(0, sw.len - sw.nq + r_last / G + 1) : sw.len;
+    const int blocks = max(0, min(take, (reach + kBlockTokens - 1) / kBlockTokens - j0));
+    const int steps = (blocks + 1) / 2;
+    const int count = steps > wt ? (steps - wt + WT - 1) / WT : 0;  // my steps
+
+    // my row g
+    const int r = r_first + g;
+    const bool valid = r < rows;
+    const int qi = valid ? r / G : 0, qh = head * G + (valid ? r % G : 0);
+    const int see = valid && a.causal ? sw.len - sw.nq + qi + 1 : sw.len;
+    int see_min = see;
 #pragma unroll
-      for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k * WR + rw][ri]);
-      float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-      for (int k = 0; k < WT; ++k) {
-        const float mk = row_m[k * WR + rw][ri];
-        if (mk != -INFINITY) sum += row_l[k * WR + rw][ri] * exp2_approx(mk - top);
-        const float4 p = *reinterpret_cast<const float4*>(
-            slabs + ((k * WR + rw) * 16 + ri) * C::SLAB_STRIDE + d);
-        v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+    for (int o = 16; o > 2; o >>= 1) see_min = min(see_min, __shfl_xor_sync(0xFFFFFFFFu, see_min, o));
+
+    // my upcoming blocks, one per lane (two to a step): row of the copy (-1: none), scales
+    const int page_blocks = a.page_tokens / kBlockTokens;
+    auto look_up = [&](int group, int& copy_row, float& sk, float& sv) {
+      const int i = 16 * group + (lane >> 1);
+      const int j = 2 * (wt + WT * i) + (lane & 1);  // of the segment's blocks
+      copy_row = -1;
+      sk = sv = 0.0f;
+      if (j >= blocks) return;
+      const int pos = (j0 + j) * kBlockTokens;
+      int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
+      if (page < 0 || page >= a.pages) {
+        raise_cache_error();
+        page = 0;
       }
-      if (whole) {
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const int qi = (r_first + r) / G, qh = head * G + (r_first + r) % G;
-        const long long at = static_cast<long long>(sw.q0 + qi) * a.q_heads + qh;
-        const __nv_bfloat162 x0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
-        const __nv_bfloat162 x1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(a.out + at * D + d) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
-        if (a.lse && d == 0)
-          a.lse[at] = sum > 0.0f ? (top - kPShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-      } else {
-        *reinterpret_cast<float4*>(dst + r * D + d) = v;
-        if (d == 0) {
-          dst[RT * D + 2 * r] = top;
-          dst[RT * D + 2 * r + 1] = sum;
+      const long long hp = static_cast<long long>(page) * a.kv_heads + head;
+      const int slot = pos % a.page_tokens;
+      copy_row = static_cast<int>(hp * a.page_tokens + slot);
+      sk = a.k_scale[hp * page_blocks + slot / kBlockTokens];
+      sv = a.v_scale[hp * page_blocks + slot / kBlockTokens];
+    };
+    int row_a, row_b;
+    float sk_a, sv_a, sk_b, sv_b;
+    look_up(0, row_a, sk_a, sv_a);
+    look_up(1, row_b, sk_b, sv_b);
+
+    auto issue = [&](int i, int consumed) {  // copies of my step i: two lanes, a block each
+      const bool cur = (i >> 4) == (consumed >> 4);
+      const int copy_row = __shfl_sync(0xFFFFFFFFu, cur ? row_a : row_b, 2 * (i & 15) + (lane & 1));
+      const int other = __shfl_xor_sync(0xFFFFFFFFu, copy_row, 1);
+      const uint32_t st = (phase + i) % STAGES;
+      if (lane == 0) mbar_arrive_expect_tx(&full[wt][st], other >= 0 ? 4 * TILE : 2 * TILE);
+      __syncwarp();
+      if (lane < 2 && copy_row >= 0) {
+        uint8_t* dst = my_ring + st * STEP + lane * TILE;
+        tma_load_2d(dst, &tm_k, &full[wt][st], 0, copy_row);
+        tma_load_2d(dst + 2 * TILE, &tm_v, &full[wt][st], 0, copy_row);
+      }
+    };
+    int issued = 0;
+    for (; issued < min(count, STAGES); ++issued) issue(issued, 0);
+
+    // q of my row as digits; channel 32t + 8s + 0..7 (D = 128; 16t + 8s for D = 64) of a
+    // row is what lane t holds of a key for matrix step s
+    uint32_t qa[KS][4], ql[KS][2];  // hi, mid, hi, mid; lo, lo
+    float qs;                       // undoes the power-of-two scaling, times the softmax scale
+    {
+      uint4 raw[KS];
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+        raw[i] = valid ? *reinterpret_cast<const uint4*>(a.q + (sw.q0 + qi) * a.q_stride +
+                                                         static_cast<long long>(qh) * D + t * (D / 4) + 8 * i)
+                       : make_uint4(0, 0, 0, 0);
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          top = fmaxf(top, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const uint32_t ex = max(__float_as_uint(top) >> 23, 21u);
+      const float up = __uint_as_float((275u - ex) << 23);  // 2^(21 - E), 2^E <= top < 2^(E + 1)
+      qs = __uint_as_float((ex - 20u) << 23) * 0.5f * a.scale_log2;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = (e & 1 ? bf16hi(w[e >> 1]) : bf16lo(w[e >> 1])) * up;
+          d[e] = (__float_as_uint(__fadd_rn(v, kRoundMagic)) - (0x4B400000u - 0x00808080u)) ^ 0x00808080u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          qa[i][2 * h] = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 2);
+          qa[i][2 * h + 1] = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 1);
+          ql[i][h] = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 0);
         }
       }
     }
+
+    float o[MD][4] = {};  // channels (D / 8) g + 2 i and + 1, queries 2t and 2t + 1
+    float m = -INFINITY, l = 0.0f;
+    float ref = 0.0f, inv_ref = 0.0f;  // power of two >= the value scales seen
+    int dead = -1;  // the step whose copies did not arrive in time
+    for (int i = 0; i < count; ++i) {
+      const uint32_t n = phase + i, st = n % STAGES;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_drain(&full[wt][st], (n / STAGES) & 1))) {
+        dead = i;
+        break;
+      }
+      const uint8_t* kt = my_ring + st * STEP;
+      const uint8_t* vt = kt + 2 * TILE;
+      float sv[2];
+      float s[2][2][2];  // [block][tile of 8 tokens][token 2t, 2t + 1]
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float f = qs * __shfl_sync(0xFFFFFFFFu, sk_a, 2 * (i & 15) + c);
+        sv[c] = __shfl_sync(0xFFFFFFFFu, sv_a, 2 * (i & 15) + c);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          int hm[4], lo[4];
+#pragma unroll
+          for (int x = 0; x < KS / 2; ++x) {
+            const int chunk = D == 128 ? 2 * t + x : t;
+            const uint4 kv =
+                *reinterpret_cast<const uint4*>(kt + c * TILE + tile_offset<D>(8 * nt + g, chunk));
+            const uint32_t la[4] = {ql[2 * x][0], 0u, ql[2 * x][1], 0u};
+            const uint32_t lb[4] = {ql[2 * x + 1][0], 0u, ql[2 * x + 1][1], 0u};
+            mma_s8(hm, qa[2 * x], kv.x, kv.y, x == 0);
+            mma_s8(lo, la, kv.x, kv.y, x == 0);
+            mma_s8(hm, qa[2 * x + 1], kv.z, kv.w, false);
+            mma_s8(lo, lb, kv.z, kv.w, false);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            s[c][nt][e] = fmaf(static_cast<float>(hm[e]), 65536.0f,
+                               static_cast<float>(hm[2 + e] * 256 + lo[e])) * f;
+        }
+      }
+      const int first = (j0 + 2 * (wt + WT * i)) * kBlockTokens;
+      if (first + 2 * kBlockTokens > min(see_min, (j0 + blocks) * kBlockTokens)) {
+        const int end = min(see, (j0 + blocks) * kBlockTokens);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (first + 16 * c + 8 * nt + 2 * t + e >= end) s[c][nt][e] = -INFINITY;
+      }
+      float top = fmaxf(fmaxf(fmaxf(s[0][0][0], s[0][0][1]), fmaxf(s[0][1][0], s[0][1][1])),
+                        fmaxf(fmaxf(s[1][0][0], s[1][0][1]), fmaxf(s[1][1][0], s[1][1][1])));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const float sv_top = fmaxf(sv[0], sv[1]);
+      if (__any_sync(0xFFFFFFFFu, sv_top > ref || top > m + kPSlack)) {
+        float shrink = 1.0f;
+        if (sv_top > ref) {
+          const uint32_t e = max(min((__float_as_uint(sv_top) >> 23) + 1u, 252u), 2u);
+          inv_ref = __uint_as_float((254u - e) << 23);
+          shrink = ref * inv_ref;
+          ref = __uint_as_float(e << 23);
+        }
+        float f = 1.0f;
+        if (top > m + kPSlack) {
+          f = exp2_approx(m - top);  // 0 for the first maximum
+          m = top;
+        }
+        l *= f;
+        const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * t) * shrink;
+        const float f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4) * shrink;
+#pragma unroll
+        for (int x = 0; x < MD; ++x) {
+          o[x][0] *= f0; o[x][1] *= f1; o[x][2] *= f0; o[x][3] *= f1;
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m - kPShift;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float wv = sv[c] * inv_ref;
+        uint32_t pf[2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float p0 = exp2_approx(s[c][nt][0] - base), p1 = exp2_approx(s[c][nt][1] - base);
+          l += p0 + p1;
+          pf[nt] = pack_half2(p0 * wv, p1 * wv);
+        }
+        // values: lane (g, t) takes 16 (8) channels of tokens 2t, 2t+1, 2t+8, 2t+9
+        uint32_t vw[4][D / 32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vt + c * TILE + tile_offset<D>(tok, g));
+            vw[k][0] = v.x; vw[k][1] = v.y; vw[k][2] = v.z; vw[k][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(
+                vt + c * TILE + tile_offset<D>(tok, g >> 1) + 8 * (g & 1));
+            vw[k][0] = v.x; vw[k][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = vw[k][w] ^ 0x80808080u;
+          const uint32_t lo0 = __byte_perm(v[0], v[1], 0x5140), hi0 = __byte_perm(v[0], v[1], 0x7362);
+          const uint32_t lo1 = __byte_perm(v[2], v[3], 0x5140), hi1 = __byte_perm(v[2], v[3], 0x7362);
+          mma_f16(o[2 * w], bytes_f16x2(lo0, 0x4140), bytes_f16x2(lo0, 0x4342),
+                  bytes_f16x2(lo1, 0x4140), bytes_f16x2(lo1, 0x4342), pf[0], pf[1]);
+          mma_f16(o[2 * w + 1], bytes_f16x2(hi0, 0x4140), bytes_f16x2(hi0, 0x4342),
+                  bytes_f16x2(hi1, 0x4140), bytes_f16x2(hi1, 0x4342), pf[0], pf[1]);
+        }
+      }
+      __syncwarp();  // the stage has been read
+      if (issued < count) {
+        issue(issued, i);
+        ++issued;
+      }
+      if ((i & 15) == 15) {
+        row_a = row_b; sk_a = sk_b; sv_a = sv_b;
+        look_up((i >> 4) + 2, row_b, sk_b, sv_b);
+      }
+    }
+    if (dead >= 0 && lane == 0)  // wait (bounded) for the copies in flight
+      for (int i = dead; i < issued; ++i)
+        mbar_wait_drain(&full[wt][(phase + i) % STAGES], ((phase + i) / STAGES) & 1);
+    phase += count;
+
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+    if (t == 0) {
+      row_m[wt][g] = m;
+      row_l[wt][g] = l;
+    }
+    __syncthreads();  // also: every ring is drained, the slabs may lie over them
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k][g]);
+    const float f = m == -INFINITY ? 0.0f : exp2_approx(m - top) * ref;
+    const float fq[2] = {__shfl_sync(0xFFFFFFFFu, f, 8 * t), __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4)};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float* dst = slabs + (wt * RT + 2 * t + e) * (D + 4) + g * (D / 8);
+#pragma unroll
+      for (int x = 0; x < MD; x += 2)
+        *reinterpret_cast<float4*>(dst + 2 * x) =
+            make_float4(o[x][e] * fq[e], o[x][2 + e] * fq[e], o[x + 1][e] * fq[e], o[x + 1][2 + e] * fq[e]);
+    }
+    __syncthreads();
+    attn_finish<D, 1, RT>(a, sw, row_m, row_l, slabs, r_first, head, j0 == 0 && take == sw.blocks,
+                          j0 == 0);
+    // the next copies write where the slabs were read and written by ordinary accesses
+    fence_proxy_async_smem();
     if (__syncthreads_or(dead >= 0)) return;  // the error word is set
     u += take;
     rem += take;
@@ -755,12 +1116,15 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
 
 // ------------------------------------------------------------ host side
 
-// Row-warps of a tile: as many as the average sequence's rows per cache head need, up to
-// four (a tile of 64 rows reads each block once for all of them).
-int attn_row_warps(int Tq, int B, int q_heads, int kv_heads) {
+// Rows of a tile, by the rows per cache head that an average sequence has: 8 (its own
+// kernel), or 16 to a warp and as many warps side by side as the rows need, up to four (a
+// tile of 64 rows reads each block once for all of them).
+int attn_tile_rows(int Tq, int B, int q_heads, int kv_heads) {
   const long long rows = static_cast<long long>(Tq) * (q_heads / kv_heads);
-  return rows <= 16LL * B ? 1 : rows <= 32LL * B ? 2 : 4;
+  return rows <= 8LL * B ? 8 : rows <= 16LL * B ? 16 : rows <= 32LL * B ? 32 : 64;
 }
+
+constexpr int kAttnMaxCtas = 3;  // per SM, of any instance
 
 size_t attn_prefix_bytes(int B) { return (8 * (static_cast<size_t>(B) + 1) + 255) / 256 * 256; }
 
@@ -777,17 +1141,33 @@ bool cache_map(CUtensorMap* m, const void* base, int D, long long rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int WR>
-cudaError_t run_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int grid,
-                     cudaStream_t st) {
-  using C = AttnCfg<D, WR>;
-  static std::atomic<bool> done[kAttrDevices];
-  const cudaError_t e = set_smem_once(attn_kv8_kernel<D, WR>, C::SMEM, done);
+template <class Kernel>
+cudaError_t run_attn(Kernel kernel, std::atomic<bool> (&done)[kAttrDevices], int smem, int ctas,
+                     const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int D,
+                     int RT, cudaStream_t st) {
+  const cudaError_t e = set_smem_once(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  const cudaError_t f = launch_pdl(attn_kv8_kernel<D, WR>, grid, 32 * kAttnWarps, C::SMEM, st, 1,
-                                   tm_k, tm_v, a);
+  const int grid = sm_count() * ctas;
+  const cudaError_t f = launch_pdl(kernel, grid, 32 * kAttnWarps, smem, st, 1, tm_k, tm_v, a);
   if (f != cudaSuccess) return f;
-  return launch_pdl(attn_kv8_join_kernel<D>, a.Tq * a.q_heads, 128, 0, st, 1, a, grid, C::RT);
+  return launch_pdl(D == 128 ? attn_kv8_join_kernel<128> : attn_kv8_join_kernel<64>,
+                    a.Tq * a.q_heads, 128, 0, st, 1, a, grid, RT);
+}
+
+template <int D>
+cudaError_t dispatch_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a,
+                          int RT, cudaStream_t st) {
+  static std::atomic<bool> done[4][kAttrDevices];
+#define WQ_ATTN(I_, CFG_, KERNEL_) \
+  return run_attn(KERNEL_, done[I_], CFG_::SMEM, CFG_::CTAS, tm_k, tm_v, a, D, RT, st)
+  using C1 = AttnCfg<D, 1>;
+  using C2 = AttnCfg<D, 2>;
+  using C4 = AttnCfg<D, 4>;
+  if (RT == 8) WQ_ATTN(0, AttnFewCfg<D>, attn_kv8_few_kernel<D>);
+  if (RT == 16) WQ_ATTN(1, C1, (attn_kv8_kernel<D, 1>));
+  if (RT == 32) WQ_ATTN(2, C2, (attn_kv8_kernel<D, 2>));
+  WQ_ATTN(3, C4, (attn_kv8_kernel<D, 4>));
+#undef WQ_ATTN
 }
 
 }  // namespace
@@ -809,8 +1189,8 @@ cudaError_t launch_kv8_append(const Kv8Append& p, cudaStream_t st) {
 }
 
 size_t attn_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int D) {
-  const size_t rt = 16 * attn_row_warps(Tq, B, q_heads, kv_heads);
-  const size_t grid = static_cast<size_t>(sm_count()) * kAttnCtasPerSm;
+  const size_t rt = attn_tile_rows(Tq, B, q_heads, kv_heads);
+  const size_t grid = static_cast<size_t>(sm_count()) * kAttnMaxCtas;
   return attn_prefix_bytes(B) + (grid * 2 * rt * (D + 2) * 4 + 255) / 256 * 256;
 }
 
@@ -829,15 +1209,9 @@ cudaError_t launch_attn_kv8(const Kv8Attn& p, cudaStream_t st) {
   a.Tq = p.Tq; a.B = p.cache.B; a.q_heads = p.q_heads; a.kv_heads = p.cache.kv_heads;
   a.max_pages = p.cache.max_pages; a.pages = p.cache.pages; a.page_tokens = p.cache.page_tokens;
   a.causal = p.causal; a.scale_log2 = p.scale * 1.4426950408889634f;
-  const int grid = sm_count() * kAttnCtasPerSm;
-  const int wr = attn_row_warps(p.Tq, p.cache.B, p.q_heads, p.cache.kv_heads);
-#define WQ_ATTN(D_)                                                          \
-  return wr == 1   ? run_attn<D_, 1>(tm_k, tm_v, a, grid, st)                \
-         : wr == 2 ? run_attn<D_, 2>(tm_k, tm_v, a, grid, st)                \
-                   : run_attn<D_, 4>(tm_k, tm_v, a, grid, st)
-  if (p.cache.D == 128) WQ_ATTN(128);
-  WQ_ATTN(64);
-#undef WQ_ATTN
+  const int rt = attn_tile_rows(p.Tq, p.cache.B, p.q_heads, p.cache.kv_heads);
+  return p.cache.D == 128 ? dispatch_attn<128>(tm_k, tm_v, a, rt, st)
+                          : dispatch_attn<64>(tm_k, tm_v, a, rt, st);
 }
 
 }  // namespace wq
