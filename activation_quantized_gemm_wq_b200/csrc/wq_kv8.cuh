@@ -379,46 +379,54 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
 }
 
 // One CTA of four warps takes an equal share of all units (so ragged batches stay
-// balanced and one long sequence fills the GPU), item by item.  WR warps cover the rows
-// of a tile (16 each), the other factor 4 / WR of the warps take the blocks in turn.
-// Each such token group has its own ring of STAGES blocks (16 x D keys and values), filled
-// by bulk tensor copies that its first warp issues, so the warps run independently
-// between the ends of items.  Codes become f16 in registers, exactly; q enters as f16
-// after a power-of-two scaling per row that keeps all its 8 bits; scores, maxima, sums
-// and the output are fp32.  Block scales multiply the scores (keys) and the softmax
-// weights relative to a power-of-two reference (values).
-template <int D, int WR>
+// balanced and one long sequence fills the GPU), item by item.  WR warps cover the rows of
+// a tile, 16 MT each (with MT = 2 a code is made f16 once for 32 rows), the other factor
+// 4 / WR of the warps take steps of two blocks in turn.  Each such token group has its own
+// ring of steps, filled by bulk tensor copies that its first warp issues, so the warps run
+// independently between the ends of items.  Codes become f16 in registers, exactly; q
+// enters as f16 after a power-of-two scaling per row that keeps all its 8 bits; scores,
+// maxima, sums and the output are fp32.  Block scales multiply the scores (keys) and the
+// softmax weights relative to a power-of-two reference (values).
+template <int D, int MT, int WR>
 struct AttnCfg {
   static constexpr int WT = kAttnWarps / WR;   // token groups
-  static constexpr int RT = 16 * WR;           // rows per tile
+  static constexpr int ROWS = 16 * MT;         // of a warp
+  static constexpr int RT = ROWS * WR;         // of a tile
   static constexpr int TILE = kBlockTokens * D;
-  static constexpr int STAGES = 65536 / (WT * 2 * TILE) < 8 ? 65536 / (WT * 2 * TILE) : 8;
-  static constexpr int RING = WT * STAGES * 2 * TILE;
-  static constexpr int SLAB_STRIDE = D + 4;
-  static constexpr int SLABS = kAttnWarps * 16 * SLAB_STRIDE * 4;
-  static constexpr int SMEM = RING + SLABS + 1024;  // + alignment
-  static constexpr int CTAS = D == 128 ? 2 : 3;     // per SM
+  static constexpr int STEP = 4 * TILE;        // two blocks of keys and values
+  static constexpr int STAGES = D == 128 && WT == 4 ? 2 : 3;
+  static constexpr bool QREG = MT * D <= 128;  // q stays in registers, else in shared memory
+  static constexpr int RING = WT * STAGES * STEP;
+  static constexpr int SLABS = kAttnWarps * ROWS * (D + 4) * 4;  // over the ring
+  static constexpr int QBYTES = QREG ? 0 : kAttnWarps * ROWS * D * 2;
+  static constexpr int SMEM = (RING > SLABS ? RING : SLABS) + QBYTES + 1024;  // + alignment
+  static constexpr int CTAS = MT == 1 && D == 64 ? 3 : 2;                     // per SM
 };
 
-template <int D, int WR>
-__global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, WR>::CTAS) attn_kv8_kernel(
+template <int D, int MT, int WR>
+__global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) attn_kv8_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const AttnArgs a) {
-  using C = AttnCfg<D, WR>;
-  constexpr int WT = C::WT, RT = C::RT, STAGES = C::STAGES, TILE = C::TILE;
+  using C = AttnCfg<D, MT, WR>;
+  constexpr int WT = C::WT, ROWS = C::ROWS, RT = C::RT, STAGES = C::STAGES, TILE = C::TILE;
+  constexpr int STEP = C::STEP;
+  constexpr bool QREG = C::QREG;
   constexpr int KS = D / 16;   // matrix steps over the channels
   constexpr int ND = D / 8;    // 8-channel tiles of the output
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* slabs = reinterpret_cast<float*>(ring + C::RING);
+  float* slabs = reinterpret_cast<float*>(ring);
   __shared__ __align__(8) uint64_t full[WT][STAGES], empty[WT][STAGES];
-  __shared__ float row_m[kAttnWarps][16], row_l[kAttnWarps][16];
+  __shared__ float row_m[kAttnWarps][ROWS], row_l[kAttnWarps][ROWS];
   __shared__ AttnSched sched;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wt = warp / WR, wr = warp % WR;
   const int G = a.q_heads / a.kv_heads;
-  uint8_t* my_ring = ring + wt * STAGES * 2 * TILE;
+  uint8_t* my_ring = ring + wt * STAGES * STEP;
+  // [step over the channels][16-row half][lane] operands, a copy per warp
+  uint4* q_smem = reinterpret_cast<uint4*>(ring + (C::RING > C::SLABS ? C::RING : C::SLABS)) +
+                  warp * (QREG ? 0 : KS * MT * 32) + lane;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < WT; ++i)
@@ -432,54 +440,39 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, WR>::CTAS) attn_kv
   }
   griddep_wait();
   griddep_launch_dependents();
-
   const AttnShare share = attn_share<RT>(a, sched);
   if (share.begin >= share.end) return;
 
   int b = share.b;
   long long rem = share.rem;
-  const long long u_begin = share.begin, u_end = share.end;
-  uint32_t phase = 0;  // blocks this token group has taken so far (stage and parity)
+  uint32_t phase = 0;  // steps this token group has taken so far (stage and parity)
   SeqWork sw = sequence_work<RT>(a, b, false);
-  for (long long u = u_begin; u < u_end;) {
+  for (long long u = share.begin; u < share.end;) {
     while (rem >= sw.units) {  // the next sequence that has any work
       rem = 0;
       sw = sequence_work<RT>(a, ++b, false);
     }
     const long long item = rem / sw.blocks;
     const int j0 = static_cast<int>(rem % sw.blocks);
-    const int take = static_cast<int>(min(static_cast<long long>(sw.blocks - j0), u_end - u));
+    const int take = static_cast<int>(min(static_cast<long long>(sw.blocks - j0), share.end - u));
     const int head = static_cast<int>(item / sw.tiles), tile = static_cast<int>(item % sw.tiles);
     const int rows = sw.nq * G;
     const int r_first = tile * RT, r_last = min(r_first + RT, rows) - 1;
     // tokens that the tile's last row sees, which no earlier row exceeds
     const int reach = a.causal ? max(0, sw.len - sw.nq + r_last / G + 1) : sw.len;
-    const int j1 = min(j0 + take, (reach + kBlockTokens - 1) / kBlockTokens);
-    const int count = j1 - j0 > wt ? (j1 - j0 - wt + WT - 1) / WT : 0;  // my blocks
+    const int blocks = max(0, min(take, (reach + kBlockTokens - 1) / kBlockTokens - j0));
+    const int steps = (blocks + 1) / 2;
+    const int count = steps > wt ? (steps - wt + WT - 1) / WT : 0;  // my steps
 
-    // my rows: g and g + 8 of the warp's sixteen
-    int see[2];
-    const uint16_t* qp[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = r_first + 16 * wr + 8 * h + g;
-      const bool valid = r < rows;
-      const int qi = valid ? r / G : 0, qh = head * G + (valid ? r % G : 0);
-      see[h] = valid && a.causal ? sw.len - sw.nq + qi + 1 : sw.len;
-      qp[h] = valid ? a.q + (sw.q0 + qi) * a.q_stride + static_cast<long long>(qh) * D : nullptr;
-    }
-    int see_min = min(see[0], see[1]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) see_min = min(see_min, __shfl_xor_sync(0xFFFFFFFFu, see_min, o));
-
-    // upcoming blocks of this group, one per lane: row of the copy, scales
-    const long long cap_blocks = a.page_tokens / kBlockTokens;
+    // my upcoming blocks, one per lane (two to a step): row of the copy (-1: none), scales
+    const int page_blocks = a.page_tokens / kBlockTokens;
     auto look_up = [&](int group, int& copy_row, float& sk, float& sv) {
-      const int i = 32 * group + lane;
-      copy_row = 0;
+      const int i = 16 * group + (lane >> 1);
+      const int j = 2 * (wt + WT * i) + (lane & 1);  // of the segment's blocks
+      copy_row = -1;
       sk = sv = 0.0f;
-      if (i >= count) return;
-      const int pos = (j0 + wt + WT * i) * kBlockTokens;
+      if (j >= blocks) return;
+      const int pos = (j0 + j) * kBlockTokens;
       int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
       if (page < 0 || page >= a.pages) {
         raise_cache_error();
@@ -488,50 +481,60 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, WR>::CTAS) attn_kv
       const long long hp = static_cast<long long>(page) * a.kv_heads + head;
       const int slot = pos % a.page_tokens;
       copy_row = static_cast<int>(hp * a.page_tokens + slot);
-      sk = a.k_scale[hp * cap_blocks + slot / kBlockTokens];
-      sv = a.v_scale[hp * cap_blocks + slot / kBlockTokens];
+      sk = a.k_scale[hp * page_blocks + slot / kBlockTokens];
+      sv = a.v_scale[hp * page_blocks + slot / kBlockTokens];
     };
     int row_a, row_b;
     float sk_a, sv_a, sk_b, sv_b;
     look_up(0, row_a, sk_a, sv_a);
     look_up(1, row_b, sk_b, sv_b);
 
-    auto issue = [&](int i, int consumed) {  // copies of my block i
-      const bool cur = (i >> 5) == (consumed >> 5);
-      const int copy_row = __shfl_sync(0xFFFFFFFFu, cur ? row_a : row_b, i & 31);
+    auto issue = [&](int i, int consumed) {  // copies of my step i: two lanes, a block each
+      const bool cur = (i >> 4) == (consumed >> 4);
+      const int copy_row = __shfl_sync(0xFFFFFFFFu, cur ? row_a : row_b, 2 * (i & 15) + (lane & 1));
+      const int other = __shfl_xor_sync(0xFFFFFFFFu, copy_row, 1);
       if (wr == 0) {
         const uint32_t n = phase + i, st = n % STAGES, round = n / STAGES;
         bool ok = true;
         if (WR > 1 && round > 0) ok = mbar_wait_drain(&empty[wt][st], (round - 1) & 1);
-        if (lane == 0 && ok) {
-          mbar_arrive_expect_tx(&full[wt][st], 2 * TILE);
-          tma_load_2d(my_ring + st * 2 * TILE, &tm_k, &full[wt][st], 0, copy_row);
-          tma_load_2d(my_ring + st * 2 * TILE + TILE, &tm_v, &full[wt][st], 0, copy_row);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (lane == 0 && ok) mbar_arrive_expect_tx(&full[wt][st], other >= 0 ? 4 * TILE : 2 * TILE);
+        __syncwarp();
+        if (lane < 2 && ok && copy_row >= 0) {
+          uint8_t* dst = my_ring + st * STEP + lane * TILE;
+          tma_load_2d(dst, &tm_k, &full[wt][st], 0, copy_row);
+          tma_load_2d(dst + 2 * TILE, &tm_v, &full[wt][st], 0, copy_row);
         }
       }
       __syncwarp();
     };
-    const int ahead = min(count, STAGES);
-    for (int i = 0; i < ahead; ++i) issue(i, 0);
+    int issued = 0;
+    for (; issued < min(count, STAGES); ++issued) issue(issued, 0);
 
-    // q of my rows as f16 operands; channel 32t' + 16s + 4w + 0..3 (D = 128; 16t + 4w for
-    // D = 64) of a row is what lane t's word w of its load s holds of a key
-    uint32_t qf[KS][4];
-    float qs[2];  // undoes the rows' power-of-two scaling, times the softmax scale
-    {
-      uint4 raw[2][D / 32];
+    // my rows: g and g + 8 of each sixteen.  q as f16 operands: channel 32t + 16x + 4w + 0..3
+    // (D = 128; 16t + 4w for D = 64) of a row is what lane t's word w of its load x holds of
+    // a key
+    int see[MT][2], see_min = 0x7FFFFFFF;
+    float qs[MT][2];  // undoes the rows' power-of-two scaling, times the softmax scale
+    uint32_t qf[QREG ? KS : 1][MT][4];
+    __syncwarp();  // the last item's operands in shared memory have been read
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          raw[h][i] = qp[h] ? *reinterpret_cast<const uint4*>(qp[h] + t * (D / 4) + 8 * i)
-                            : make_uint4(0, 0, 0, 0);
+    for (int mt = 0; mt < MT; ++mt) {
+      uint32_t f[KS][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const int r = r_first + ROWS * wr + 16 * mt + 8 * h + g;
+        const bool valid = r < rows;
+        const int qi = valid ? r / G : 0, qh = head * G + (valid ? r % G : 0);
+        see[mt][h] = valid && a.causal ? sw.len - sw.nq + qi + 1 : sw.len;
+        see_min = min(see_min, see[mt][h]);
+        const uint16_t* qp = a.q + (sw.q0 + qi) * a.q_stride + static_cast<long long>(qh) * D + t * (D / 4);
+        uint4 raw[D / 32];
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+          raw[i] = valid ? *reinterpret_cast<const uint4*>(qp + 8 * i) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             top = fmaxf(top, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
@@ -541,25 +544,42 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, WR>::CTAS) attn_kv
         // the largest value of the row comes to lie in [2^14, 2^15)
         const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
         const float up = __uint_as_float((268u - e) << 23);
-        qs[h] = __uint_as_float((e - 14u) << 23) * a.scale_log2;
+        qs[mt][h] = __uint_as_float((e - 14u) << 23) * a.scale_log2;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
           for (int e2 = 0; e2 < 4; ++e2)
-            qf[2 * i + (e2 >> 1)][h + 2 * (e2 & 1)] =
-                pack_half2(bf16lo(w[e2]) * up, bf16hi(w[e2]) * up);
+            f[2 * i + (e2 >> 1)][h + 2 * (e2 & 1)] = pack_half2(bf16lo(w[e2]) * up, bf16hi(w[e2]) * up);
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if constexpr (QREG) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[ks][mt][e] = f[ks][e];
+        } else {
+          q_smem[(ks * MT + mt) * 32] = make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
         }
       }
     }
+    __syncwarp();
+#pragma unroll
+    for (int x = 16; x > 2; x >>= 1) see_min = min(see_min, __shfl_xor_sync(0xFFFFFFFFu, see_min, x));
 
-    float o[ND][4] = {};
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float o[MT][ND][4] = {};
+    float m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        m[mt][h] = -INFINITY;
+        l[mt][h] = 0.0f;
+      }
     float ref = 0.0f, inv_ref = 0.0f;  // power of two >= the value scales seen
-    int dead = -1;  // the block whose copy did not arrive in time
-    int issued = ahead;
-    // a stage is refilled when its readers are done: at once where there is one reader,
-    // one block later where several warps share it, so that none waits for the slowest
+    int dead = -1;  // the step whose copies did not arrive in time
+    // a stage is refilled when its readers are done: at once where there is one reader, one
+    // step later where several warps share it, so that none waits for the slowest
     constexpr int LAG = WR > 1 ? 1 : 0;
     for (int i = 0; i < count; ++i) {
       const uint32_t n = phase + i, st = n % STAGES;
@@ -567,128 +587,166 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, WR>::CTAS) attn_kv
         dead = i;
         break;
       }
-      const uint8_t* kt = my_ring + st * 2 * TILE;
-      const uint8_t* vt = kt + TILE;
-      const float sk = __shfl_sync(0xFFFFFFFFu, sk_a, i & 31);
-      const float sv = __shfl_sync(0xFFFFFFFFu, sv_a, i & 31);
+      const uint8_t* kt = my_ring + st * STEP;
+      const uint8_t* vt = kt + 2 * TILE;
 
-      // scores of 16 tokens: columns of the two tiles are tokens 0-7 and 8-15
-      float s[2][4] = {};
+      // scores of 32 tokens: column tiles 2c, 2c + 1 are tokens 0-7 and 8-15 of block c
+      float s[MT][4][4] = {};
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
+      for (int x = 0; x < D / 64; ++x) {
+        const int chunk = D == 128 ? 2 * t + x : t;
+        uint4 kv[4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int chunk = D == 128 ? 2 * t + c : t;
-          const uint4 kv = *reinterpret_cast<const uint4*>(kt + tile_offset<D>(8 * nt + g, chunk));
-          const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+        for (int nt = 0; nt < 4; ++nt)
+          kv[nt] = *reinterpret_cast<const uint4*>(kt + (nt >> 1) * TILE +
+                                                   tile_offset<D>(8 * (nt & 1) + g, chunk));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t u = w[e] ^ 0x80808080u;
-            const uint32_t (&f)[4] = qf[4 * c + e];
-            mma_f16(s[nt], f[0], f[1], f[2], f[3], bytes_f16x2(u, 0x4140), bytes_f16x2(u, 0x4342));
+        for (int e = 0; e < 4; ++e) {
+          uint4 f[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            if constexpr (QREG)
+              f[mt] = make_uint4(qf[4 * x + e][mt][0], qf[4 * x + e][mt][1], qf[4 * x + e][mt][2],
+                                 qf[4 * x + e][mt][3]);
+            else
+              f[mt] = q_smem[((4 * x + e) * MT + mt) * 32];
+          }
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const uint32_t w = word_of(kv[nt], e) ^ 0x80808080u;
+            const uint32_t b0 = bytes_f16x2(w, 0x4140), b1 = bytes_f16x2(w, 0x4342);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              mma_f16(s[mt][nt], f[mt].x, f[mt].y, f[mt].z, f[mt].w, b0, b1);
           }
         }
-      // values: lane (g, t) takes 16 (8) channels of tokens 2t, 2t+1, 2t+8, 2t+9
-      uint32_t vw[4][D / 32];
+      }
+
+      float sk[2], sv[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
-        if constexpr (D == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(vt + tile_offset<D>(tok, g));
-          vw[k][0] = v.x; vw[k][1] = v.y; vw[k][2] = v.z; vw[k][3] = v.w;
-        } else {
-          const uint2 v =
-              *reinterpret_cast<const uint2*>(vt + tile_offset<D>(tok, g >> 1) + 8 * (g & 1));
-          vw[k][0] = v.x; vw[k][1] = v.y;
+      for (int c = 0; c < 2; ++c) {
+        sk[c] = __shfl_sync(0xFFFFFFFFu, sk_a, 2 * (i & 15) + c);
+        sv[c] = __shfl_sync(0xFFFFFFFFu, sv_a, 2 * (i & 15) + c);
+      }
+      const int first = (j0 + 2 * (wt + WT * i)) * kBlockTokens;
+      const int last = (j0 + blocks) * kBlockTokens;
+      const bool cut = first + 2 * kBlockTokens > min(see_min, last);
+      const float sv_top = fmaxf(sv[0], sv[1]);
+      bool grow = sv_top > ref;
+      float top[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float f[2] = {qs[mt][h] * sk[0], qs[mt][h] * sk[1]};
+          float mx = -INFINITY;
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[mt][nt][2 * h + e] *= f[nt >> 1];
+          if (cut) {
+            const int end = min(see[mt][h], last);
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (first + 8 * nt + 2 * t + e >= end) s[mt][nt][2 * h + e] = -INFINITY;
+          }
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][2 * h], s[mt][nt][2 * h + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+          top[mt][h] = mx;
+          grow |= mx > m[mt][h] + kPSlack;
+        }
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        float shrink = 1.0f;
+        if (sv_top > ref) {
+          const uint32_t e = max(min((__float_as_uint(sv_top) >> 23) + 1u, 252u), 2u);
+          inv_ref = __uint_as_float((254u - e) << 23);
+          shrink = ref * inv_ref;
+          ref = __uint_as_float(e << 23);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float f = 1.0f;
+            if (top[mt][h] > m[mt][h] + kPSlack) {
+              f = exp2_approx(m[mt][h] - top[mt][h]);  // 0 for the first maximum
+              m[mt][h] = top[mt][h];
+            }
+            l[mt][h] *= f;
+            f *= shrink;
+#pragma unroll
+            for (int nd = 0; nd < ND; ++nd) {
+              o[mt][nd][2 * h] *= f;
+              o[mt][nd][2 * h + 1] *= f;
+            }
+          }
+      }
+      uint32_t pf[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float base = m[mt][h] == -INFINITY ? 0.0f : m[mt][h] - kPShift;
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const float wv = sv[nt >> 1] * inv_ref;
+            const float p0 = exp2_approx(s[mt][nt][2 * h] - base);
+            const float p1 = exp2_approx(s[mt][nt][2 * h + 1] - base);
+            l[mt][h] += p0 + p1;
+            pf[mt][nt >> 1][2 * (nt & 1) + h] = pack_half2(p0 * wv, p1 * wv);
+          }
+        }
+      // o += p v.  Lane (g, t) takes 16 (8) channels of tokens 2t, 2t+1, 2t+8, 2t+9; 4 x 4
+      // bytes (four tokens, four channels) give four tiles' operands
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t vw[4][D / 32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vt + c * TILE + tile_offset<D>(tok, g));
+            vw[k][0] = v.x; vw[k][1] = v.y; vw[k][2] = v.z; vw[k][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(
+                vt + c * TILE + tile_offset<D>(tok, g >> 1) + 8 * (g & 1));
+            vw[k][0] = v.x; vw[k][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = vw[k][w] ^ 0x80808080u;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t x0 = __byte_perm(v[0], v[1], half ? 0x7362 : 0x5140);
+            const uint32_t x1 = __byte_perm(v[2], v[3], half ? 0x7362 : 0x5140);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t b0 = bytes_f16x2(x0, e ? 0x4342 : 0x4140);
+              const uint32_t b1 = bytes_f16x2(x1, e ? 0x4342 : 0x4140);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma_f16(o[mt][4 * w + 2 * half + e], pf[mt][c][0], pf[mt][c][1], pf[mt][c][2],
+                        pf[mt][c][3], b0, b1);
+            }
+          }
         }
       }
-      // the stage is in registers: refill it
-      __syncwarp();
+      __syncwarp();  // the stage has been read
       if (WR > 1 && lane == 0) mbar_arrive(&empty[wt][st]);
       if (issued < count && issued < i + 1 + STAGES - LAG) {
         issue(issued, i);
         ++issued;
       }
-
-      const int first = (j0 + wt + WT * i) * kBlockTokens;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] *= qs[e >> 1] * sk;
-      if (first + kBlockTokens > see_min) {
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (first + 8 * nt + 2 * t + (e & 1) >= see[e >> 1]) s[nt][e] = -INFINITY;
-      }
-      float top[2];
-      bool grow = sv > ref;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 1));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 2));
-        grow |= top[h] > m[h] + kPSlack;
-      }
-      if (__any_sync(0xFFFFFFFFu, grow)) {
-        float shrink = 1.0f;
-        if (sv > ref) {
-          const uint32_t e = min((__float_as_uint(sv) >> 23) + 1u, 252u);
-          const float to = __uint_as_float(max(e, 2u) << 23);
-          inv_ref = __uint_as_float((254u - max(e, 2u)) << 23);
-          shrink = ref * inv_ref;
-          ref = to;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float f = 1.0f;
-          if (top[h] > m[h] + kPSlack) {
-            f = exp2_approx(m[h] - top[h]);  // 0 for the first maximum
-            m[h] = top[h];
-          }
-          l[h] *= f;
-          f *= shrink;
-#pragma unroll
-          for (int nd = 0; nd < ND; ++nd) {
-            o[nd][2 * h] *= f;
-            o[nd][2 * h + 1] *= f;
-          }
-        }
-      }
-      const float wv = sv * inv_ref;
-      uint32_t pf[2][2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float base = m[h] == -INFINITY ? 0.0f : m[h] - kPShift;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const float p0 = exp2_approx(s[nt][2 * h] - base);
-          const float p1 = exp2_approx(s[nt][2 * h + 1] - base);
-          l[h] += p0 + p1;
-          pf[nt][h] = pack_half2(p0 * wv, p1 * wv);
-        }
-      }
-      // o += p v: 4 x 4 bytes (four tokens, four channels) give four tiles' operands
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        uint32_t u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = vw[k][w] ^ 0x80808080u;
-        const uint32_t lo0 = __byte_perm(u[0], u[1], 0x5140), hi0 = __byte_perm(u[0], u[1], 0x7362);
-        const uint32_t lo1 = __byte_perm(u[2], u[3], 0x5140), hi1 = __byte_perm(u[2], u[3], 0x7362);
-        mma_f16(o[4 * w], pf[0][0], pf[0][1], pf[1][0], pf[1][1], bytes_f16x2(lo0, 0x4140),
-                bytes_f16x2(lo1, 0x4140));
-        mma_f16(o[4 * w + 1], pf[0][0], pf[0][1], pf[1][0], pf[1][1], bytes_f16x2(lo0, 0x4342),
-                bytes_f16x2(lo1, 0x4342));
-        mma_f16(o[4 * w + 2], pf[0][0], pf[0][1], pf[1][0], pf[1][1], bytes_f16x2(hi0, 0x4140),
-                bytes_f16x2(hi1, 0x4140));
-        mma_f16(o[4 * w + 3], pf[0][0], pf[0][1], pf[1][0], pf[1][1], bytes_f16x2(hi0, 0x4342),
-                bytes_f16x2(hi1, 0x4342));
-      }
-      if ((i & 31) == 31) {
+      if ((i & 15) == 15) {
         row_a = row_b; sk_a = sk_b; sv_a = sv_b;
-        look_up((i >> 5) + 2, row_b, sk_b, sv_b);
+        look_up((i >> 4) + 2, row_b, sk_b, sv_b);
       }
     }
     if (dead >= 0 && wr == 0 && lane == 0)  // wait (bounded) for the copies in flight
@@ -696,36 +754,42 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, WR>::CTAS) attn_kv
         mbar_wait_drain(&full[wt][(phase + i) % STAGES], ((phase + i) / STAGES) & 1);
     phase += count;
 
-    // join the token groups: sums relative to the largest maximum, in group order
+    // join the token groups
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
-      if (t == 0) {
-        row_m[warp][8 * h + g] = m[h];
-        row_l[warp][8 * h + g] = l[h];
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][h], 1);
+        l[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][h], 2);
+        if (t == 0) {
+          row_m[warp][16 * mt + 8 * h + g] = m[mt][h];
+          row_l[warp][16 * mt + 8 * h + g] = l[mt][h];
+        }
       }
-    }
+    __syncthreads();  // also: every ring is drained, the slabs may lie over them
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * mt + 8 * h + g;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < WT; ++i) top = fmaxf(top, row_m[i * WR + wr][row]);
+        const float f = m[mt][h] == -INFINITY ? 0.0f : exp2_approx(m[mt][h] - top) * ref;
+        float* dst = slabs + (warp * ROWS + row) * (D + 4) + t * (D / 4);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int nd = 0; nd < ND; nd += 4)
+            *reinterpret_cast<float4*>(dst + part * ND + nd) = make_float4(
+                o[mt][nd][2 * h + part] * f, o[mt][nd + 1][2 * h + part] * f,
+                o[mt][nd + 2][2 * h + part] * f, o[mt][nd + 3][2 * h + part] * f);
+      }
     __syncthreads();
-    float* slab = slabs + warp * 16 * C::SLAB_STRIDE;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < WT; ++i) top = fmaxf(top, row_m[i * WR + wr][8 * h + g]);
-      const float f = m[h] == -INFINITY ? 0.0f : exp2_approx(m[h] - top) * ref;
-      float* dst = slab + (8 * h + g) * C::SLAB_STRIDE + t * (D / 4);
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int nd = 0; nd < ND; nd += 4)
-          *reinterpret_cast<float4*>(dst + part * ND + nd) =
-              make_float4(o[nd][2 * h + part] * f, o[nd + 1][2 * h + part] * f,
-                          o[nd + 2][2 * h + part] * f, o[nd + 3][2 * h + part] * f);
-    }
-    __syncthreads();
-    attn_finish<D, WR, 16>(a, sw, row_m, row_l, slabs, r_first, head,
-                           j0 == 0 && take == sw.blocks, j0 == 0);
+    attn_finish<D, WR, ROWS>(a, sw, row_m, row_l, slabs, r_first, head,
+                             j0 == 0 && take == sw.blocks, j0 == 0);
+    // the next copies write where the slabs were read and written by ordinary accesses
+    fence_proxy_async_smem();
     if (__syncthreads_or(dead >= 0)) return;  // the error word is set
     u += take;
     rem += take;
@@ -1117,8 +1181,7 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
 // ------------------------------------------------------------ host side
 
 // Rows of a tile, by the rows per cache head that an average sequence has: 8 (its own
-// kernel), or 16 to a warp and as many warps side by side as the rows need, up to four (a
-// tile of 64 rows reads each block once for all of them).
+// kernel), 16 or 32 (one warp wide), or 64 (two warps of 32 side by side).
 int attn_tile_rows(int Tq, int B, int q_heads, int kv_heads) {
   const long long rows = static_cast<long long>(Tq) * (q_heads / kv_heads);
   return rows <= 8LL * B ? 8 : rows <= 16LL * B ? 16 : rows <= 32LL * B ? 32 : 64;
@@ -1160,13 +1223,13 @@ cudaError_t dispatch_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, cons
   static std::atomic<bool> done[4][kAttrDevices];
 #define WQ_ATTN(I_, CFG_, KERNEL_) \
   return run_attn(KERNEL_, done[I_], CFG_::SMEM, CFG_::CTAS, tm_k, tm_v, a, D, RT, st)
-  using C1 = AttnCfg<D, 1>;
-  using C2 = AttnCfg<D, 2>;
-  using C4 = AttnCfg<D, 4>;
+  using C16 = AttnCfg<D, 1, 1>;
+  using C32 = AttnCfg<D, 2, 1>;
+  using C64 = AttnCfg<D, 2, 2>;
   if (RT == 8) WQ_ATTN(0, AttnFewCfg<D>, attn_kv8_few_kernel<D>);
-  if (RT == 16) WQ_ATTN(1, C1, (attn_kv8_kernel<D, 1>));
-  if (RT == 32) WQ_ATTN(2, C2, (attn_kv8_kernel<D, 2>));
-  WQ_ATTN(3, C4, (attn_kv8_kernel<D, 4>));
+  if (RT == 16) WQ_ATTN(1, C16, (attn_kv8_kernel<D, 1, 1>));
+  if (RT == 32) WQ_ATTN(2, C32, (attn_kv8_kernel<D, 2, 1>));
+  WQ_ATTN(3, C64, (attn_kv8_kernel<D, 2, 2>));
 #undef WQ_ATTN
 }
 
