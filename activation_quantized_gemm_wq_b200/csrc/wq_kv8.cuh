@@ -333,11 +333,11 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, AttnSched& sh
 // The end of a segment: the token groups' sums are joined relative to the largest maximum,
 // in group order, and written as the result, or as a partial one where other CTAs have a
 // part of the item.  In shared memory: row_m, row_l [warp][ROWS] maxima and sums of the
-// warps' rows, slabs [warp][ROWS][D + 4] their outputs, already relative to that maximum.
+// warps' rows, slabs[warp] [ROWS][D + 4] their outputs, already relative to that maximum.
 template <int D, int WR, int ROWS>
 __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw,
                                             const float (*row_m)[ROWS], const float (*row_l)[ROWS],
-                                            const float* slabs, int r_first, int head, bool whole,
+                                            const float* const* slabs, int r_first, int head, bool whole,
                                             bool from_start) {
   constexpr int WT = kAttnWarps / WR, RT = ROWS * WR;
   const int G = a.q_heads / a.kv_heads, rows = sw.nq * G;
@@ -355,7 +355,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
       const float mk = row_m[k * WR + rw][ri];
       if (mk != -INFINITY) sum += row_l[k * WR + rw][ri] * exp2_approx(mk - top);
       const float4 p = *reinterpret_cast<const float4*>(
-          slabs + ((k * WR + rw) * ROWS + ri) * (D + 4) + d);
+          slabs[k * WR + rw] + ri * (D + 4) + d);
       v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
     }
     if (whole) {
@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
   float* slabs = reinterpret_cast<float*>(ring);
   __shared__ __align__(8) uint64_t full[WT][STAGES], empty[WT][STAGES];
   __shared__ float row_m[kAttnWarps][ROWS], row_l[kAttnWarps][ROWS];
+  __shared__ const float* slab_at[kAttnWarps];
   __shared__ AttnSched sched;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  if (lane == 0) slab_at[warp] = slabs + warp * ROWS * (D + 4);
   griddep_wait();
   griddep_launch_dependents();
   const AttnShare share = attn_share<RT>(a, sched);
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
                 o[mt][nd + 2][2 * h + part] * f, o[mt][nd + 3][2 * h + part] * f);
       }
     __syncthreads();
-    attn_finish<D, WR, ROWS>(a, sw, row_m, row_l, slabs, r_first, head,
+    attn_finish<D, WR, ROWS>(a, sw, row_m, row_l, slab_at, r_first, head,
                              j0 == 0 && take == sw.blocks, j0 == 0);
     // the next copies write where the slabs were read and written by ordinary accesses
     fence_proxy_async_smem();
@@ -800,37 +802,41 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
 // head): the same work in fewer instructions, which is what bounds it.
 // Scores come from the integer matrix instructions, with the cached codes as they are: q
 // becomes 22-bit integers relative to its row's largest value (off by at most 2^-22 of
-// it), three signed bytes hi, mid, lo; rows 0 to 7 of one operand are hi, 8 to 15 mid, so
-// that a lane holds both sums, and a second operand has lo.  Sums over the channels are
-// exact.  A lane then holds the scores of row g for tokens 2t, 2t + 1, which is the layout
-// that the transposed product o^T += v^T p^T wants of p^T: half the instructions and
-// accumulators of o += p v, of whose sixteen rows eight would be empty.
+// it), three signed bytes hi, mid, lo.  For RT = 8, rows 0 to 7 of one operand are hi, 8 to
+// 15 mid, so that a lane holds both sums, and a second operand has lo; for RT = 4, one
+// operand has hi (rows 0 to 3), mid (4 to 7) and lo (8 to 11), and mid is fetched from
+// another lane.  Sums over the channels are exact.  A lane then holds the scores of row g for
+// tokens 2t, 2t + 1, which is the layout that the transposed product o^T += v^T p^T wants
+// of p^T: half the instructions and accumulators of o += p v, of whose sixteen rows eight
+// would be empty.
 // A step is two blocks (32 tokens): the maxima, the reference and the barrier are looked
-// at once for both.
-template <int D>
+// at once for both.  The first step of the next segment is fetched while this one's sums
+// are joined (in the other stage of each warp's ring).
+template <int D, int RT_>
 struct AttnFewCfg {
-  static constexpr int RT = 8, WT = kAttnWarps, TILE = kBlockTokens * D;
+  static constexpr int RT = RT_, WT = kAttnWarps, TILE = kBlockTokens * D;
   static constexpr int STEP = 4 * TILE;               // two blocks of keys and values
-  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int STAGES = 2;
   static constexpr int RING = WT * STAGES * STEP;
-  static constexpr int SLABS = kAttnWarps * RT * (D + 4) * 4;
-  static constexpr int SMEM = RING + 1024;            // + alignment; the slabs lie over the ring
-  static constexpr int CTAS = 3;
+  static constexpr int SMEM = RING + 1024;            // + alignment
+  static constexpr int CTAS = D == 128 ? 3 : 4;
+  static_assert(RT * (D + 4) * 4 <= STEP, "a warp's sums fit one stage");
 };
 
-template <int D>
-__global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D>::CTAS) attn_kv8_few_kernel(
+template <int D, int RT_>
+__global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) attn_kv8_few_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const AttnArgs a) {
-  using C = AttnFewCfg<D>;
+  using C = AttnFewCfg<D, RT_>;
   constexpr int WT = C::WT, RT = C::RT, STAGES = C::STAGES, TILE = C::TILE, STEP = C::STEP;
   constexpr int KS = D / 32;   // matrix steps over the channels
   constexpr int MD = D / 16;   // 16-channel tiles of the transposed output
+  constexpr bool FOUR = RT == 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* slabs = reinterpret_cast<float*>(ring);
   __shared__ __align__(8) uint64_t full[WT][STAGES];
   __shared__ float row_m[kAttnWarps][RT], row_l[kAttnWarps][RT];
+  __shared__ const float* slab_at[kAttnWarps];
   __shared__ AttnSched sched;
 
   const int wt = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -850,79 +856,85 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D>::CTAS) attn_kv8
   if (share.begin >= share.end) return;
 
   int b = share.b;
-  long long rem = share.rem;
-  uint32_t phase = 0;  // steps this warp has taken so far (stage and parity)
+  long long rem = share.rem, u = share.begin;
+  uint32_t phase = 0;  // steps this warp has taken before this segment (stage and parity)
   SeqWork sw = sequence_work<RT>(a, b, false);
-  for (long long u = share.begin; u < share.end;) {
+
+  // The segment at (b, rem): part of an item's blocks
+  int j0, take, head, r_first, blocks, count;
+  int row_a, row_b;  // my upcoming blocks, one per lane (two to a step): row of the copy (-1: none),
+  float sk_a, sv_a, sk_b, sv_b;  // and scales; now and next
+  const int page_blocks = a.page_tokens / kBlockTokens;
+  auto look_up = [&](int group, int& copy_row, float& sk, float& sv) {
+    const int i = 16 * group + (lane >> 1);
+    const int j = 2 * (wt + WT * i) + (lane & 1);  // of the segment's blocks
+    copy_row = -1;
+    sk = sv = 0.0f;
+    if (j >= blocks) return;
+    const int pos = (j0 + j) * kBlockTokens;
+    int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
+    if (page < 0 || page >= a.pages) {
+      raise_cache_error();
+      page = 0;
+    }
+    const long long hp = static_cast<long long>(page) * a.kv_heads + head;
+    const int slot = pos % a.page_tokens;
+    copy_row = static_cast<int>(hp * a.page_tokens + slot);
+    sk = a.k_scale[hp * page_blocks + slot / kBlockTokens];
+    sv = a.v_scale[hp * page_blocks + slot / kBlockTokens];
+  };
+  auto issue = [&](int i, int consumed) {  // copies of my step i: two lanes, a block each
+    const bool cur = (i >> 4) == (consumed >> 4);
+    const int copy_row = __shfl_sync(0xFFFFFFFFu, cur ? row_a : row_b, 2 * (i & 15) + (lane & 1));
+    const int other = __shfl_xor_sync(0xFFFFFFFFu, copy_row, 1);
+    const uint32_t st = (phase + i) % STAGES;
+    if (lane == 0) mbar_arrive_expect_tx(&full[wt][st], other >= 0 ? 4 * TILE : 2 * TILE);
+    __syncwarp();
+    if (lane < 2 && copy_row >= 0) {
+      uint8_t* dst = my_ring + st * STEP + lane * TILE;
+      tma_load_2d(dst, &tm_k, &full[wt][st], 0, copy_row);
+      tma_load_2d(dst + 2 * TILE, &tm_v, &full[wt][st], 0, copy_row);
+    }
+  };
+  auto begin_segment = [&]() {
     while (rem >= sw.units) {  // the next sequence that has any work
       rem = 0;
       sw = sequence_work<RT>(a, ++b, false);
     }
     const long long item = rem / sw.blocks;
-    const int j0 = static_cast<int>(rem % sw.blocks);
-    const int take = static_cast<int>(min(static_cast<long long>(sw.blocks - j0), share.end - u));
-    const int head = static_cast<int>(item / sw.tiles), tile = static_cast<int>(item % sw.tiles);
-    const int rows = sw.nq * G;
-    const int r_first = tile * RT, r_last = min(r_first + RT, rows) - 1;
+    j0 = static_cast<int>(rem % sw.blocks);
+    take = static_cast<int>(min(static_cast<long long>(sw.blocks - j0), share.end - u));
+    head = static_cast<int>(item / sw.tiles);
+    r_first = static_cast<int>(item % sw.tiles) * RT;
+    const int r_last = min(r_first + RT, sw.nq * G) - 1;
+    // tokens that the tile's last row sees, which no earlier row exceeds
     const int reach = a.causal ? max(0, sw.len - sw.nq + r_last / G + 1) : sw.len;
-    const int blocks = max(0, min(take, (reach + kBlockTokens - 1) / kBlockTokens - j0));
+    blocks = max(0, min(take, (reach + kBlockTokens - 1) / kBlockTokens - j0));
     const int steps = (blocks + 1) / 2;
-    const int count = steps > wt ? (steps - wt + WT - 1) / WT : 0;  // my steps
+    count = steps > wt ? (steps - wt + WT - 1) / WT : 0;  // my steps
+    look_up(0, row_a, sk_a, sv_a);
+    look_up(1, row_b, sk_b, sv_b);
+    if (count > 0) issue(0, 0);
+  };
+  begin_segment();
 
-    // my row g
-    const int r = r_first + g;
-    const bool valid = r < rows;
+  for (;;) {
+    int issued = min(count, 1);
+    for (; issued < min(count, STAGES); ++issued) issue(issued, 0);
+
+    // my row
+    const int r = r_first + (FOUR ? g & 3 : g);
+    const bool valid = r < sw.nq * G;
     const int qi = valid ? r / G : 0, qh = head * G + (valid ? r % G : 0);
     const int see = valid && a.causal ? sw.len - sw.nq + qi + 1 : sw.len;
     int see_min = see;
 #pragma unroll
     for (int o = 16; o > 2; o >>= 1) see_min = min(see_min, __shfl_xor_sync(0xFFFFFFFFu, see_min, o));
 
-    // my upcoming blocks, one per lane (two to a step): row of the copy (-1: none), scales
-    const int page_blocks = a.page_tokens / kBlockTokens;
-    auto look_up = [&](int group, int& copy_row, float& sk, float& sv) {
-      const int i = 16 * group + (lane >> 1);
-      const int j = 2 * (wt + WT * i) + (lane & 1);  // of the segment's blocks
-      copy_row = -1;
-      sk = sv = 0.0f;
-      if (j >= blocks) return;
-      const int pos = (j0 + j) * kBlockTokens;
-      int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
-      if (page < 0 || page >= a.pages) {
-        raise_cache_error();
-        page = 0;
-      }
-      const long long hp = static_cast<long long>(page) * a.kv_heads + head;
-      const int slot = pos % a.page_tokens;
-      copy_row = static_cast<int>(hp * a.page_tokens + slot);
-      sk = a.k_scale[hp * page_blocks + slot / kBlockTokens];
-      sv = a.v_scale[hp * page_blocks + slot / kBlockTokens];
-    };
-    int row_a, row_b;
-    float sk_a, sv_a, sk_b, sv_b;
-    look_up(0, row_a, sk_a, sv_a);
-    look_up(1, row_b, sk_b, sv_b);
-
-    auto issue = [&](int i, int consumed) {  // copies of my step i: two lanes, a block each
-      const bool cur = (i >> 4) == (consumed >> 4);
-      const int copy_row = __shfl_sync(0xFFFFFFFFu, cur ? row_a : row_b, 2 * (i & 15) + (lane & 1));
-      const int other = __shfl_xor_sync(0xFFFFFFFFu, copy_row, 1);
-      const uint32_t st = (phase + i) % STAGES;
-      if (lane == 0) mbar_arrive_expect_tx(&full[wt][st], other >= 0 ? 4 * TILE : 2 * TILE);
-      __syncwarp();
-      if (lane < 2 && copy_row >= 0) {
-        uint8_t* dst = my_ring + st * STEP + lane * TILE;
-        tma_load_2d(dst, &tm_k, &full[wt][st], 0, copy_row);
-        tma_load_2d(dst + 2 * TILE, &tm_v, &full[wt][st], 0, copy_row);
-      }
-    };
-    int issued = 0;
-    for (; issued < min(count, STAGES); ++issued) issue(issued, 0);
-
-    // q of my row as digits; channel 32t + 8s + 0..7 (D = 128; 16t + 8s for D = 64) of a
-    // row is what lane t holds of a key for matrix step s
-    uint32_t qa[KS][4], ql[KS][2];  // hi, mid, hi, mid; lo, lo
-    float qs;                       // undoes the power-of-two scaling, times the softmax scale
+    // its q as digits; channel 32t + 8s + 0..7 (D = 128; 16t + 8s for D = 64) of a row is
+    // what lane t holds of a key for matrix step s
+    uint32_t qa[KS][4], ql[FOUR ? 1 : KS][2];  // RT = 8: hi, mid, hi, mid; lo, lo
+    float qs;                                  // undoes the power-of-two scaling, times the softmax scale
     {
       uint4 raw[KS];
 #pragma unroll
@@ -942,7 +954,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D>::CTAS) attn_kv8
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       const uint32_t ex = max(__float_as_uint(top) >> 23, 21u);
       const float up = __uint_as_float((275u - ex) << 23);  // 2^(21 - E), 2^E <= top < 2^(E + 1)
-      qs = __uint_as_float((ex - 20u) << 23) * 0.5f * a.scale_log2;
+      qs = FOUR && g >= 4 ? 0.0f : __uint_as_float((ex - 20u) << 23) * 0.5f * a.scale_log2;
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -954,9 +966,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D>::CTAS) attn_kv8
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          qa[i][2 * h] = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 2);
-          qa[i][2 * h + 1] = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 1);
-          ql[i][h] = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 0);
+          const uint32_t hi = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 2);
+          const uint32_t mid = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 1);
+          const uint32_t low = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 0);
+          qa[i][2 * h] = FOUR && g >= 4 ? mid : hi;
+          qa[i][2 * h + 1] = FOUR ? low : mid;
+          if constexpr (!FOUR) ql[i][h] = low;
         }
       }
     }
@@ -987,17 +1002,22 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D>::CTAS) attn_kv8
             const int chunk = D == 128 ? 2 * t + x : t;
             const uint4 kv =
                 *reinterpret_cast<const uint4*>(kt + c * TILE + tile_offset<D>(8 * nt + g, chunk));
-            const uint32_t la[4] = {ql[2 * x][0], 0u, ql[2 * x][1], 0u};
-            const uint32_t lb[4] = {ql[2 * x + 1][0], 0u, ql[2 * x + 1][1], 0u};
             mma_s8(hm, qa[2 * x], kv.x, kv.y, x == 0);
-            mma_s8(lo, la, kv.x, kv.y, x == 0);
             mma_s8(hm, qa[2 * x + 1], kv.z, kv.w, false);
-            mma_s8(lo, lb, kv.z, kv.w, false);
+            if constexpr (!FOUR) {
+              const uint32_t la[4] = {ql[2 * x][0], 0u, ql[2 * x][1], 0u};
+              const uint32_t lb[4] = {ql[2 * x + 1][0], 0u, ql[2 * x + 1][1], 0u};
+              mma_s8(lo, la, kv.x, kv.y, x == 0);
+              mma_s8(lo, lb, kv.z, kv.w, false);
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int e = 0; e < 2; ++e) {
+            const int mid = FOUR ? __shfl_xor_sync(0xFFFFFFFFu, hm[e], 16) : hm[2 + e];
+            const int low = FOUR ? hm[2 + e] : lo[e];
             s[c][nt][e] = fmaf(static_cast<float>(hm[e]), 65536.0f,
-                               static_cast<float>(hm[2 + e] * 256 + lo[e])) * f;
+                               static_cast<float>(mid * 256 + low)) * f;
+          }
         }
       }
       const int first = (j0 + 2 * (wt + WT * i)) * kBlockTokens;
@@ -1092,102 +1112,145 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D>::CTAS) attn_kv8
 
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    if (t == 0) {
+    if (t == 0 && g < RT) {
       row_m[wt][g] = m;
       row_l[wt][g] = l;
     }
-    __syncthreads();  // also: every ring is drained, the slabs may lie over them
+    // on to the next segment: its first copies go to the stage `phase` names, this one's
+    // sums to the other (of the warp's own ring, whose stages have all been read)
+    const SeqWork sw_now = sw;
+    const int head_now = head, r_now = r_first;
+    const bool whole = j0 == 0 && take == sw.blocks, from_start = j0 == 0;
+    u += take;
+    rem += take;
+    const bool more = u < share.end && __all_sync(0xFFFFFFFFu, dead < 0);
+    float* slab = reinterpret_cast<float*>(my_ring + (phase + 1) % STAGES * STEP);
+    if (more) begin_segment();
+    __syncthreads();
     float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k][g]);
+    for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k][FOUR ? g & 3 : g]);
     const float f = m == -INFINITY ? 0.0f : exp2_approx(m - top) * ref;
     const float fq[2] = {__shfl_sync(0xFFFFFFFFu, f, 8 * t), __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4)};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float* dst = slabs + (wt * RT + 2 * t + e) * (D + 4) + g * (D / 8);
+      if (2 * t + e >= RT) break;
+      float* dst = slab + (2 * t + e) * (D + 4) + g * (D / 8);
 #pragma unroll
       for (int x = 0; x < MD; x += 2)
         *reinterpret_cast<float4*>(dst + 2 * x) =
             make_float4(o[x][e] * fq[e], o[x][2 + e] * fq[e], o[x + 1][e] * fq[e], o[x + 1][2 + e] * fq[e]);
     }
+    if (lane == 0) slab_at[wt] = slab;
     __syncthreads();
-    attn_finish<D, 1, RT>(a, sw, row_m, row_l, slabs, r_first, head, j0 == 0 && take == sw.blocks,
-                          j0 == 0);
-    // the next copies write where the slabs were read and written by ordinary accesses
+    attn_finish<D, 1, RT>(a, sw_now, row_m, row_l, slab_at, r_now, head_now, whole, from_start);
+    // the next copies write where the sums were written and read by ordinary accesses
     fence_proxy_async_smem();
-    if (__syncthreads_or(dead >= 0)) return;  // the error word is set
-    u += take;
-    rem += take;
+    if (__syncthreads_or(dead >= 0)) {  // the error word is set
+      if (more && count > 0 && lane == 0)
+        mbar_wait_drain(&full[wt][phase % STAGES], (phase / STAGES) & 1);
+      return;
+    }
+    if (!more) return;
   }
 }
 
-// Joins the partial results of items that several CTAs shared, in CTA order; a CTA per
-// query row and head, which returns at once where one CTA had the whole item.
+// Joins the partial results of items that several CTAs shared.  Such an item has a CTA's
+// end inside it: kJoinSplit CTAs of this kernel look at the end of each CTA of the first
+// one, and all that look at ends inside one item share its outputs among them.  As many
+// lanes as there are parts (a power of two, at most a warp) take one four of outputs, so
+// that every load is in flight at once; they are added as a tree, the same every time.
+constexpr int kJoinSplit = 4;
+
 template <int D>
 __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, int grid, int RT) {
-  __shared__ float part[4][D + 2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x / a.q_heads, qh = blockIdx.x % a.q_heads;
   griddep_wait();
   griddep_launch_dependents();
-  const int b = find_sequence(a.q_start, a.B, row);
-  if (b < 0) return;
+  const long long total = a.prefix[a.B];
+  const long long per = units_per_cta(total, grid);
+  const long long cut = per * (blockIdx.x / kJoinSplit + 1);
+  if (cut >= total) return;
+  // the sequence that unit `cut` belongs to: the last b with prefix[b] <= cut
+  const int lane = threadIdx.x & 31;
+  int b = 0;
+  for (int span = a.B; span > 1;) {
+    const int step = (span + 31) / 32;
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, lane * step < span && a.prefix[b + (lane * step < span ? lane * step : 0)] <= cut);
+    const int k = hit ? 31 - __clz(hit) : 0;
+    span = min(step, span - k * step);
+    b += k * step;
+  }
   const int G = a.q_heads / a.kv_heads;
   const int q0 = min(max(a.q_start[b], 0), a.Tq), nq = max(min(a.q_start[b + 1], a.Tq) - q0, 0);
-  if (row < q0 || row >= q0 + nq) return;
-  const long long units = a.prefix[b + 1] - a.prefix[b], total = a.prefix[a.B];
+  const long long before = a.prefix[b], units = a.prefix[b + 1] - before;
   const int tiles = static_cast<int>((static_cast<long long>(nq) * G + RT - 1) / RT);
+  if (tiles == 0) return;
   const long long blocks = units / (static_cast<long long>(tiles) * a.kv_heads);
-  const int r = (row - q0) * G + qh % G;
-  const long long u0 = a.prefix[b] + (static_cast<long long>(qh / G) * tiles + r / RT) * blocks;
-  const long long per = units_per_cta(total, grid);
+  const long long item = (cut - before) / blocks, u0 = before + item * blocks;
+  if (u0 == cut) return;  // a CTA ends where an item does
   const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + blocks - 1) / per);
-  if (c0 == c1) return;
-  const int ri = r % RT;
+  const int head = static_cast<int>(item / tiles), r_first = static_cast<int>(item % tiles) * RT;
+  const int rows = min(RT, nq * G - r_first);
   const long long size = static_cast<long long>(RT) * (D + 2);
-  auto slot = [&](int c) {
-    return a.partial + (2LL * c + (static_cast<long long>(c) * per > u0 ? 0 : 1)) * size;
-  };
-
-  float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, slot(c)[RT * D + 2 * ri]);
-  top = warp_max(top);
-  float acc[D / 32] = {}, sum = 0.0f;
-  if (top != -INFINITY) {
-#pragma unroll 4
-    for (int c = c0 + warp; c <= c1; c += 4) {
-      const float* p = slot(c);
-      const float f = exp2_approx(p[RT * D + 2 * ri] - top);  // 0 for an empty part
-      sum += p[RT * D + 2 * ri + 1] * f;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] += p[ri * D + lane * (D / 32) + e] * f;
+  int lanes = 2;  // to an output
+  while (lanes < 32 && lanes <= c1 - c0) lanes *= 2;
+  // my piece of the outputs, in fours
+  const int all = rows * (D / 4), pieces = (c1 - c0) * kJoinSplit;
+  const int my = blockIdx.x - c0 * kJoinSplit, end = all * (my + 1) / pieces;
+  for (int base = all * my / pieces; base < end; base += 128 / lanes) {
+    const int i = min(base + static_cast<int>(threadIdx.x) / lanes, end - 1);
+    const int r = i / (D / 4), d = 4 * (i % (D / 4));
+    float top = -INFINITY, sum = 0.0f;
+    float4 v = make_float4(0, 0, 0, 0);
+    for (int c = c0 + lane % lanes; c <= c1; c += lanes) {
+      const float* p = a.partial + (2LL * c + (static_cast<long long>(c) * per > u0 ? 0 : 1)) * size;
+      const float2 ml = *reinterpret_cast<const float2*>(p + RT * D + 2 * r);
+      const float4 x = *reinterpret_cast<const float4*>(p + r * D + d);
+      const float to = fmaxf(top, ml.x);
+      if (to == -INFINITY) continue;  // empty parts
+      const float f = exp2_approx(top - to), e = exp2_approx(ml.x - to);
+      sum = sum * f + ml.y * e;
+      v.x = v.x * f + x.x * e; v.y = v.y * f + x.y * e;
+      v.z = v.z * f + x.z * e; v.w = v.w * f + x.w * e;
+      top = to;
     }
+    float all_top = top;
+    for (int o = lanes / 2; o > 0; o >>= 1)
+      all_top = fmaxf(all_top, __shfl_xor_sync(0xFFFFFFFFu, all_top, o));
+    const float f = top == -INFINITY ? 0.0f : exp2_approx(top - all_top);
+    top = all_top;
+    sum *= f;
+    v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+    for (int o = lanes / 2; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+      v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+      v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, o);
+      v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, o);
+    }
+    if (lane % lanes != 0 || base + static_cast<int>(threadIdx.x) / lanes >= end) continue;
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int qi = (r_first + r) / G, qh = head * G + (r_first + r) % G;
+    const long long at = static_cast<long long>(q0 + qi) * a.q_heads + qh;
+    const __nv_bfloat162 x0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+    const __nv_bfloat162 x1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2*>(a.out + at * D + d) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
+    if (a.lse && d == 0)
+      a.lse[at] = sum > 0.0f ? (top - kPShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) part[warp][lane * (D / 32) + e] = acc[e];
-  if (lane == 0) part[warp][D] = sum;
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= D) return;
-  const float all = part[0][D] + part[1][D] + part[2][D] + part[3][D];
-  const float v = part[0][d] + part[1][d] + part[2][d] + part[3][d];
-  const long long at = static_cast<long long>(row) * a.q_heads + qh;
-  a.out[at * D + d] =
-      __bfloat16_as_ushort(__float2bfloat16_rn(all > 0.0f ? v / all : 0.0f));
-  if (a.lse && d == 0)
-    a.lse[at] = all > 0.0f ? (top - kPShift + log2f(all)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------ host side
 
-// Rows of a tile, by the rows per cache head that an average sequence has: 8 (its own
-// kernel), 16 or 32 (one warp wide), or 64 (two warps of 32 side by side).
+// Rows of a tile, by the rows per cache head that an average sequence has: 4 or 8 (their
+// own kernel), 16 or 32 (one warp wide), or 64 (two warps of 32 side by side).
 int attn_tile_rows(int Tq, int B, int q_heads, int kv_heads) {
   const long long rows = static_cast<long long>(Tq) * (q_heads / kv_heads);
-  return rows <= 8LL * B ? 8 : rows <= 16LL * B ? 16 : rows <= 32LL * B ? 32 : 64;
+  return rows <= 4LL * B ? 4 : rows <= 8LL * B ? 8 : rows <= 16LL * B ? 16 : rows <= 32LL * B ? 32 : 64;
 }
 
-constexpr int kAttnMaxCtas = 3;  // per SM, of any instance
+constexpr int kAttnMaxCtas = 4;  // per SM, of any instance
 
 size_t attn_prefix_bytes(int B) { return (8 * (static_cast<size_t>(B) + 1) + 255) / 256 * 256; }
 
@@ -1214,19 +1277,22 @@ cudaError_t run_attn(Kernel kernel, std::atomic<bool> (&done)[kAttrDevices], int
   const cudaError_t f = launch_pdl(kernel, grid, 32 * kAttnWarps, smem, st, 1, tm_k, tm_v, a);
   if (f != cudaSuccess) return f;
   return launch_pdl(D == 128 ? attn_kv8_join_kernel<128> : attn_kv8_join_kernel<64>,
-                    a.Tq * a.q_heads, 128, 0, st, 1, a, grid, RT);
+                    (grid - 1) * kJoinSplit, 128, 0, st, 1, a, grid, RT);
 }
 
 template <int D>
 cudaError_t dispatch_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a,
                           int RT, cudaStream_t st) {
-  static std::atomic<bool> done[4][kAttrDevices];
+  static std::atomic<bool> done[5][kAttrDevices];
 #define WQ_ATTN(I_, CFG_, KERNEL_) \
   return run_attn(KERNEL_, done[I_], CFG_::SMEM, CFG_::CTAS, tm_k, tm_v, a, D, RT, st)
   using C16 = AttnCfg<D, 1, 1>;
   using C32 = AttnCfg<D, 2, 1>;
   using C64 = AttnCfg<D, 2, 2>;
-  if (RT == 8) WQ_ATTN(0, AttnFewCfg<D>, attn_kv8_few_kernel<D>);
+  using C4 = AttnFewCfg<D, 4>;
+  using C8 = AttnFewCfg<D, 8>;
+  if (RT == 4) WQ_ATTN(4, C4, (attn_kv8_few_kernel<D, 4>));
+  if (RT == 8) WQ_ATTN(0, C8, (attn_kv8_few_kernel<D, 8>));
   if (RT == 16) WQ_ATTN(1, C16, (attn_kv8_kernel<D, 1, 1>));
   if (RT == 32) WQ_ATTN(2, C32, (attn_kv8_kernel<D, 2, 1>));
   WQ_ATTN(3, C64, (attn_kv8_kernel<D, 2, 2>));
