@@ -503,7 +503,8 @@ wq_status wq_pack_int4_group(const wq_bf16* W, const float* c, int N, int K, int
                              uint8_t* qw, wq_bf16* s_g, wq_stream_t stream) {
   WQ_TRY(check_group(group));
   WQ_TRY(check_mk(0, K));
-  if (N < 1 || static_cast<long long>(N) * K / 8 / 256 > kMaxGrid - 1) return WQ_ERR_SHAPE;
+  if (N < 1 || (static_cast<long long>(N) + 15) / 16 * ((K + 511) / 512) > kMaxGrid)
+    return WQ_ERR_SHAPE;
   if (!W || !qw || !s_g) return WQ_ERR_NULL;
   if (!aligned16(W) || !aligned16(qw) || !aligned(s_g, 2) || (c && !aligned16(c)))
     return WQ_ERR_ALIGN;
@@ -536,7 +537,7 @@ wq_status wq_kv8_append(const wq_bf16* k, const wq_bf16* v, int64_t k_stride, in
   if (T == 0 || B == 0) return WQ_OK;
   WQ_TRY(check_rows(k_stride, kv_heads, head_dim));
   WQ_TRY(check_rows(v_stride, kv_heads, head_dim));
-  if ((static_cast<long long>(T) * kv_heads * 2 + 3) / 4 > kMaxGrid) return WQ_ERR_SHAPE;
+  if (static_cast<long long>(T) * kv_heads >= 1LL << 30) return WQ_ERR_SHAPE;
   if (!k || !v || !row_start || !past_len || !block_table || !k_codes || !v_codes || !k_scale ||
       !v_scale)
     return WQ_ERR_NULL;

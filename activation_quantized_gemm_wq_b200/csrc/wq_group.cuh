@@ -23,60 +23,144 @@
 namespace wq {
 namespace {
 
+// Eight codes rint_half_even(fl(v / s)) for scales of plain_scale(), where no quotient
+// rounds beyond the code range, so that nothing has to be clamped; r = 1 / s, correctly
+// rounded.  The quotient without a division or a branch, two values at a time: t = v * r,
+// improved once with its remainder v - t s, is within one last place; then, by Markstein's
+// theorem (Computation of elementary functions on the IBM RISC System/6000 processor, 1990),
+// adding its remainder, which is exact, times r gives the correctly rounded fl(v / s).  The low
+// bits of a result are the code.  (quantize8_recip's margin around half-integers takes one
+// operation less, but sends an eighth of the warps the long way: packing 16384 x 4096 took
+// 62.9 us so, 49.3 us this way.)
+__device__ __forceinline__ void quantize8_pairs(const float2 (&v)[4], float s, float r,
+                                                uint32_t (&c)[8]) {
+  const float2 rr = make_float2(r, r), minus_s = make_float2(-s, -s);
+  const float2 magic = make_float2(kRoundMagic, kRoundMagic);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2 t = __fmul2_rn(v[e], rr);
+    t = __ffma2_rn(__ffma2_rn(t, minus_s, v[e]), rr, t);
+    t = __ffma2_rn(__ffma2_rn(t, minus_s, v[e]), rr, t);
+    const float2 u = __fadd2_rn(t, magic);
+    c[2 * e] = __float_as_uint(u.x);
+    c[2 * e + 1] = __float_as_uint(u.y);
+  }
+}
+
+// Scales for which quantize8_pairs holds: 1 / s is normal, a remainder of a quotient that is
+// not rounded to 0 is exact, and the scale, a maximum over QMAX, is within 2^-8 of that.
+__device__ __forceinline__ bool plain_scale(float s) { return s >= 0x1p-100f && s <= 0x1p120f; }
+
 // ------------------------------------------------------------ packing (offline)
 
-// Codes of eight channels as one word of the packed layout.
+// Codes of eight channels (in the low nibbles) as one word of the packed layout.
 __device__ __forceinline__ uint32_t group_word(const uint32_t (&c)[8]) {
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w |= (c[2 * i] & 0xFu) << (4 * i);
-    w |= (c[2 * i + 1] & 0xFu) << (4 * i + 16);
-  }
+  for (int i = 0; i < 4; ++i)
+    w |= (__byte_perm(c[2 * i], c[2 * i + 1], 0x5410) << (4 * i)) & (0x000F000Fu << (4 * i));
   return w;
 }
 
-// Thread = eight channels of one output channel; the G/8 threads of a group are
-// neighbours in a warp and share the maximum by shuffles.  W is read and the codes are
-// written once.  The scale is rounded to bf16 (2 bytes beside 16 to 64 bytes of codes)
-// BEFORE the codes are decided, so the codes belong to the scale that is stored; a
-// scale rounded down by at most 2^-9 sends the maximum to 7.03, which clamps to 7.
-template <int G>
-__global__ void __launch_bounds__(256) pack_int4_group_kernel(
-    const uint16_t* __restrict__ W, const float* __restrict__ c, int N, int K,
-    uint32_t* __restrict__ qw, uint16_t* __restrict__ s_g) {
-  const int chunks = K / 8;  // a multiple of 16
-  const size_t total = static_cast<size_t>(N) * chunks;
-  const size_t idx = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+// CTA = 512 input channels of every so many 16 output channels (a tile), the next tile's loads
+// in flight while one is packed; four threads to a run of 128 channels.
+// Thread t of a run takes channels 32j + 8t .. + 7, j = 0..3 (a quad's loads are 64
+// consecutive bytes, all four in flight): they are the words that lie next to each other in
+// the packed run, one 16-byte store.  A group is whole in the quad: its maximum is taken
+// within the threads, then by two shuffles.  W is read and the codes are written once; the
+// scales go through shared memory, so that sixteen rows' leave as one 32-byte piece.  The
+// scale is rounded to bf16 (2 bytes beside 16 to 64 bytes of codes) BEFORE the codes are
+// decided, so the codes belong to the scale that is stored; a scale rounded down by at most
+// 2^-9 sends the maximum to 7.02, which is 7.
+template <int G, bool SCALED>
+__global__ void __launch_bounds__(256, 2) pack_int4_group_kernel(
+    const uint16_t* __restrict__ W, const float* __restrict__ c, int N, int K, int strips,
+    uint4* __restrict__ qw, uint16_t* __restrict__ s_g) {
+  constexpr int GW = G / 32;  // words of a thread in a group
+  __shared__ uint16_t scales[2][512 / G][16];
+  const int row = threadIdx.x >> 4, t = threadIdx.x & 3;
+  const int run0 = blockIdx.x % strips * 4, run = run0 + ((threadIdx.x >> 2) & 3);
+  const int tiles = (N + 15) / 16, step = gridDim.x / strips;
+  const bool valid = run < K / 128;  // the same for a quad
+  const int groups = min(512, K - run0 * 128) / G;
   griddep_wait();
   griddep_launch_dependents();
-  const bool valid = idx < total;  // threads past the end still take part in the shuffles
-  const int n = static_cast<int>(idx / chunks), ch = static_cast<int>(idx % chunks);
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (valid) raw = reinterpret_cast<const uint4*>(W)[idx];
-  float ci[8], v[8];
-  load_cinv8_global(c, ch, ci);
-  scale8(raw, ci, v);
-  float amax = 0.0f;
+  uint4 raw[4] = {};
+  auto load = [&](int tile) {
+    if (!valid || tile >= tiles) return;
+    const int n = min(tile * 16 + row, N - 1);  // rows past N repeat the last one, not written
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+    for (int j = 0; j < 4; ++j)
+      raw[j] = __ldcs(reinterpret_cast<const uint4*>(W + static_cast<size_t>(n) * K) + run * 16 + 4 * j + t);
+  };
+  int tile = blockIdx.x / strips;
+  load(tile);
+  float2 cc[SCALED ? 4 : 1][4];
+  if constexpr (SCALED) {
 #pragma unroll
-  for (int o = G / 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
-  const float s = __bfloat162float(sb);
-  const float r = __frcp_rn(s);
-  uint32_t q[8];
-  if (s > 0.0f && r <= 3.0e38f) {
-    quantize8_recip<7>(v, s, r, q);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = static_cast<uint32_t>(quantize<7>(v[e], s));
+    for (int j = 0; j < 4; ++j) {
+      const float4* cp = reinterpret_cast<const float4*>(c) + 2 * (run * 16 + 4 * j + t);
+      float4 c0 = make_float4(0, 0, 0, 0), c1 = c0;
+      if (valid) {
+        c0 = __ldg(cp);
+        c1 = __ldg(cp + 1);
+      }
+      cc[j][0] = make_float2(c0.x, c0.y); cc[j][1] = make_float2(c0.z, c0.w);
+      cc[j][2] = make_float2(c1.x, c1.y); cc[j][3] = make_float2(c1.z, c1.w);
+    }
   }
-  if (!valid) return;
-  const int at = ch & 15;  // 4 j + t
-  qw[idx - at + 4 * (at & 3) + (at >> 2)] = group_word(q);
-  if ((ch & (G / 8 - 1)) == 0)
-    s_g[static_cast<size_t>(ch / (G / 8)) * N + n] = __bfloat16_as_ushort(sb);
+  for (int turn = 0; tile < tiles; tile += step, turn ^= 1) {
+    const int n0 = tile * 16;
+    const uint4 now[4] = {raw[0], raw[1], raw[2], raw[3]};
+    load(tile + step);
+    uint32_t word[4];
+#pragma unroll
+    for (int j0 = 0; j0 < 4; j0 += GW) {
+      float2 v[GW][4];
+      float amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < GW; ++j) {
+        const uint32_t w[4] = {now[j0 + j].x, now[j0 + j].y, now[j0 + j].z, now[j0 + j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][e] = make_float2(bf16lo(w[e]), bf16hi(w[e]));
+        if constexpr (SCALED) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][e] = __fmul2_rn(v[j][e], cc[j0 + j][e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(v[j][e].x), fabsf(v[j][e].y)));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
+      const float s = __bfloat162float(sb);
+      const bool plain = plain_scale(s);
+      const float r = plain ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < GW; ++j) {
+        uint32_t q[8];
+        if (plain) {
+          quantize8_pairs(v[j], s, r, q);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            q[2 * e] = static_cast<uint32_t>(quantize_exact<7>(v[j][e].x, s));
+            q[2 * e + 1] = static_cast<uint32_t>(quantize_exact<7>(v[j][e].y, s));
+          }
+        }
+        word[j0 + j] = group_word(q);
+      }
+      if (t == 0) scales[turn][(run - run0) * (128 / G) + j0 / GW][row] = __bfloat16_as_ushort(sb);
+    }
+    if (valid && n0 + row < N)
+      qw[static_cast<size_t>(n0 + row) * (K / 32) + run * 4 + t] =
+          make_uint4(word[0], word[1], word[2], word[3]);
+    __syncthreads();  // (two buffers: the next tile's barrier frees this one's)
+    for (int i = threadIdx.x; i < groups * 16; i += 256)
+      if (n0 + (i & 15) < N)
+        s_g[(static_cast<size_t>(run0) * (128 / G) + (i >> 4)) * N + n0 + (i & 15)] =
+            scales[turn][i >> 4][i & 15];
+  }
 }
 
 // ------------------------------------------------------------ matrix-vector products
@@ -674,13 +758,20 @@ cudaError_t dispatch_gemv(const uint16_t* x, const float* cinv, const uint8_t* q
 
 cudaError_t launch_pack_int4_group(const uint16_t* W, const float* c, int N, int K, int group,
                                    uint8_t* qw, uint16_t* s_g, cudaStream_t st) {
-  const int grid = static_cast<int>((static_cast<size_t>(N) * (K / 8) + 255) / 256);
-  uint32_t* q = reinterpret_cast<uint32_t*>(qw);
-  if (group == 32)
-    return launch_pdl(pack_int4_group_kernel<32>, grid, 256, 0, st, 1, W, c, N, K, q, s_g);
-  if (group == 64)
-    return launch_pdl(pack_int4_group_kernel<64>, grid, 256, 0, st, 1, W, c, N, K, q, s_g);
-  return launch_pdl(pack_int4_group_kernel<128>, grid, 256, 0, st, 1, W, c, N, K, q, s_g);
+  const int strips = (K + 511) / 512, tiles = (N + 15) / 16;
+  // two CTAs per SM, a whole number for each strip
+  int per_strip = (2 * sm_count() + strips - 1) / strips;
+  per_strip = per_strip < tiles ? per_strip : tiles;
+  uint4* q = reinterpret_cast<uint4*>(qw);
+#define WQ_PACK(G_)                                                                          \
+  return c ? launch_pdl(pack_int4_group_kernel<G_, true>, per_strip * strips, 256, 0, st, 1, W, c, \
+                        N, K, strips, q, s_g)                                                \
+           : launch_pdl(pack_int4_group_kernel<G_, false>, per_strip * strips, 256, 0, st, 1, W, c, \
+                        N, K, strips, q, s_g)
+  if (group == 32) WQ_PACK(32);
+  if (group == 64) WQ_PACK(64);
+  WQ_PACK(128);
+#undef WQ_PACK
 }
 
 cudaError_t launch_gemv_w4g(const uint16_t* x, const float* cinv, const uint8_t* qw,

@@ -58,7 +58,8 @@ struct AppendArgs {
   int8_t* codes[2];
   float* scale[2];
   int T, B, max_pages, pages, heads, page_tokens;
-  int window;  // packed rows a warp looks through for the first tokens of blocks
+  int page_shift;  // log2 of page_tokens
+  int window;      // packed rows a warp looks through for the first tokens of blocks
 };
 
 // A warp quantizes whole blocks: all new tokens of one block, one head, keys or values.
@@ -73,23 +74,23 @@ struct AppendArgs {
 // one row for decoding (a warp per new token) and 16 rows for long runs (about one block
 // per warp, and no warps that find nothing).
 template <int D>
-__global__ void __launch_bounds__(128) kv8_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(128, D == 128 ? 5 : 7) kv8_append_kernel(const AppendArgs a) {
   constexpr int TC = D / 8;                        // 8-channel chunks of a token
   constexpr int CPL = kBlockTokens * TC / 32;      // chunks per lane of a full block
   const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int windows = (a.T + a.window - 1) / a.window;
+  const uint32_t unit = blockIdx.x * 4u + (threadIdx.x >> 5);
+  const uint32_t windows = (a.T + a.window - 1) / a.window;
   griddep_wait();
   griddep_launch_dependents();
-  if (unit >= static_cast<long long>(windows) * a.heads * 2) return;
-  const int which = static_cast<int>(unit & 1);
-  const int head = static_cast<int>((unit >> 1) % a.heads);
-  const int t0 = static_cast<int>((unit >> 1) / a.heads) * a.window;
+  if (unit >= windows * a.heads * 2u) return;
+  const int which = unit & 1;
+  const int head = (unit >> 1) % static_cast<uint32_t>(a.heads);
+  const int t0 = (unit >> 1) / static_cast<uint32_t>(a.heads) * a.window;
   const int t_end = min(t0 + a.window, a.T);
-  const uint16_t* x = a.x[which];
-  int8_t* codes = a.codes[which];
-  float* scales = a.scale[which];
-  const long long stride = a.stride[which];
+  const uint16_t* x = which ? a.x[1] : a.x[0];
+  int8_t* codes = which ? a.codes[1] : a.codes[0];
+  float* scales = which ? a.scale[1] : a.scale[0];
+  const long long stride = which ? a.stride[1] : a.stride[0];
   const long long capacity = static_cast<long long>(a.max_pages) * a.page_tokens;
 
   int t = max(t0, a.row_start[0]), b = -1;
@@ -110,19 +111,19 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const AppendArgs a) {
       }
     }
     const int pos = past + (t - first);
-    const int in_block = pos % kBlockTokens;
+    const int in_block = pos & (kBlockTokens - 1);
     const int stop = min(t + kBlockTokens - in_block, last);
     if (in_block != 0 && t != first) {  // a block that an earlier row began
       t = stop;
       continue;
     }
-    const int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
+    const int page = a.table[static_cast<long long>(b) * a.max_pages + (pos >> a.page_shift)];
     if (page < 0 || page >= a.pages) {
       if (lane == 0) raise_cache_error();
       t = stop;
       continue;
     }
-    const int slot = pos % a.page_tokens - in_block;  // the block's first slot
+    const int slot = (pos & (a.page_tokens - 1)) - in_block;  // the block's first slot
     const long long hp = static_cast<long long>(page) * a.heads + head;
     int8_t* blk = codes + (hp * a.page_tokens + slot) * D;
     float* sp = scales + hp * (a.page_tokens / kBlockTokens) + slot / kBlockTokens;
@@ -147,25 +148,25 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const AppendArgs a) {
     }
     amax = warp_max(amax);
     const float s = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
-    const float r = __frcp_rn(s);
-    const bool fast = s > 0.0f && r <= 3.0e38f;
+    const bool plain = plain_scale(s);
+    const float r = plain ? __frcp_rn(s) : 0.0f;
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int c = lane + 32 * i, tok = c / TC, ch = c % TC;
       if (tok >= count) continue;
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      float v[8];
+      float2 v[4];
       uint32_t q[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = bf16lo(w[e]);
-        v[2 * e + 1] = bf16hi(w[e]);
-      }
-      if (fast) {
-        quantize8_recip<127>(v, s, r, q);
+      for (int e = 0; e < 4; ++e) v[e] = make_float2(bf16lo(w[e]), bf16hi(w[e]));
+      if (plain) {
+        quantize8_pairs(v, s, r, q);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = static_cast<uint32_t>(quantize<127>(v[e], s));
+        for (int e = 0; e < 4; ++e) {
+          q[2 * e] = static_cast<uint32_t>(quantize_exact<127>(v[e].x, s));
+          q[2 * e + 1] = static_cast<uint32_t>(quantize_exact<127>(v[e].y, s));
+        }
       }
       *reinterpret_cast<uint2*>(blk + (in_block + tok) * D + 8 * ch) =
           make_uint2(pack_low_bytes(q[0], q[1], q[2], q[3]), pack_low_bytes(q[4], q[5], q[6], q[7]));
@@ -1310,6 +1311,7 @@ cudaError_t launch_kv8_append(const Kv8Append& p, cudaStream_t st) {
   a.scale[0] = p.cache.k_scale; a.scale[1] = p.cache.v_scale;
   a.T = p.T; a.B = p.cache.B; a.max_pages = p.cache.max_pages; a.pages = p.cache.pages;
   a.heads = p.cache.kv_heads; a.page_tokens = p.cache.page_tokens;
+  a.page_shift = a.page_tokens == 16 ? 4 : a.page_tokens == 32 ? 5 : a.page_tokens == 64 ? 6 : 7;
   a.window = p.T > 16LL * a.B ? 16 : 1;
   const long long windows = (p.T + a.window - 1) / a.window;
   const int grid = static_cast<int>((windows * a.heads * 2 + 3) / 4);

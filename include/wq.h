@@ -389,7 +389,7 @@ wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
  * page are not read.  Allocating, sharing and freeing pages is the caller's: sequences
  * may share pages that are only read, but a block that is appended to must be in one
  * sequence's table only.  Limits: pages * kv_heads * page_tokens and max_pages *
- * page_tokens below 2^31.
+ * page_tokens below 2^31, T * kv_heads below 2^30.
  *
  * Appends new tokens: row r of k and v (bf16, kv_heads * head_dim elements packed
  * within a row, rows k_stride / v_stride elements apart, a multiple of 8) with
