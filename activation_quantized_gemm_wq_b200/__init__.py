@@ -109,6 +109,8 @@ _I32 = frozenset({"torch.int32"})
 _I8 = frozenset({"torch.int8"})
 
 
+_device_index = None
+_raw_stream = None
 _type_names = {}
 
 
@@ -120,8 +122,11 @@ def _type_name(dtype):
 
 
 def _current_device():
-    import torch
-    return torch.cuda.current_device()
+    global _device_index
+    if _device_index is None:   # (an import statement per call costs as much as the question)
+        import torch
+        _device_index = torch.cuda.current_device
+    return _device_index()
 
 
 def _ptr(t, name, kinds=None, count=0, device=None):
@@ -153,15 +158,16 @@ def _check(t, name, kinds, count, device):
 def _row_ptr(t, name, heads, head_dim, device):
     """Address and row stride of [rows][heads][head_dim] bf16 rows that may be part of
     wider ones (a slice of a fused q/k/v projection): packed within a row."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows, {heads}, {head_dim}]")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [rows, {heads}, {head_dim}]")
     if not t.is_cuda:
         raise ValueError(f"{name}: libwq takes device tensors")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+    rows, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != head_dim):
         raise ValueError(f"{name}: libwq takes rows that are packed within themselves")
     _check(t, name, _BF16, 0, device)
-    packed = heads * head_dim
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else packed)
+    return t.data_ptr(), (rows if shape[0] > 1 else heads * head_dim)
 
 
 def _codes_per_row(K, act_bits):
@@ -171,9 +177,12 @@ def _codes_per_row(K, act_bits):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        # the raw handle alone: building a torch Stream object costs more than a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # the raw handle alone: building a torch Stream object costs as much as a launch
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        return _raw_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -399,10 +408,11 @@ def _cache_args(k_codes, v_codes, k_scale, v_scale, block_table, B, dev):
     """The cache's pointers and sizes, checked: codes [pages][kv_heads][page_tokens][D],
     scales [pages][kv_heads][page_tokens / 16], block_table [B][max_pages]."""
     pages, heads, page_tokens, D = k_codes.shape
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table: shape {tuple(block_table.shape)}, expected [{B}, max_pages]")
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table: shape {tuple(shape)}, expected [{B}, max_pages]")
     n = pages * heads * page_tokens
-    return (_ptr(block_table, "block_table", _I32, 0, dev), block_table.shape[1],
+    return (_ptr(block_table, "block_table", _I32, 0, dev), shape[1],
             _ptr(k_codes, "k_codes", _I8, n * D, dev), _ptr(v_codes, "v_codes", _I8, n * D, dev),
             _ptr(k_scale, "k_scale", _F32, n // 16, dev),
             _ptr(v_scale, "v_scale", _F32, n // 16, dev), pages, heads, page_tokens, D)
@@ -439,8 +449,7 @@ def wq_attn_kv8(q, q_start, kv_len, block_table, k_codes, v_codes, k_scale, v_sc
     dev = _current_device()
     B = kv_len.shape[0]
     cache = _cache_args(k_codes, v_codes, k_scale, v_scale, block_table, B, dev)
-    heads, D = q.shape[1], cache[-1]
-    Tq = q.shape[0]
+    Tq, heads, D = q.shape[0], q.shape[1], cache[-1]
     qp, qs = _row_ptr(q, "q", heads, D, dev)
     _call("wq_attn_kv8", qp, qs, Tq, heads, _ptr(q_start, "q_start", _I32, B + 1, dev),
           _ptr(kv_len, "kv_len", _I32, B, dev), B, *cache, 1 if causal else 0, float(scale),

@@ -129,11 +129,8 @@ class RowT(DevT):
         super().__init__(shape, dtype, **kw)
         self._s = strides or self._t.stride()
 
-    def dim(self):
-        return self._t.dim()
-
-    def stride(self, i):
-        return self._s[i]
+    def stride(self):
+        return self._s
 
 
 M, K, N, G = 3, 256, 24, 64
