@@ -381,7 +381,7 @@ wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
 
 /* The cache.  `pages` pages of `page_tokens` (16, 32, 64 or 128) tokens each hold, per
  * head of head_dim (64 or 128) channels, int8 codes and one fp32 scale per block of 16
- * tokens, for keys and values each; a cached value is scale * code:
+ * tokens, for keys and values each; a cached value is scale * code (scale >= 0):
  *   k_codes, v_codes [pages][kv_heads][page_tokens][head_dim] int8
  *   k_scale, v_scale [pages][kv_heads][page_tokens / 16] fp32
  * Token p of sequence b lies in page block_table[b][p / page_tokens], slot
