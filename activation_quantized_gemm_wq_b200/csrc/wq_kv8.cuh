@@ -335,32 +335,147 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, AttnSched& sh
   return s;
 }
 
-// The end of a segment: the token groups' sums are joined relative to the largest maximum,
-// in group order, and written as the result, or as a partial one where other CTAs have a
-// part of the item.  In shared memory: row_m, row_l [warp][ROWS] maxima and sums of the
-// warps' rows, slabs[warp] [ROWS][D + 4] their outputs, already relative to that maximum.
-template <int D, int WR, int ROWS>
+// A warp's way through a CTA's share: segments, each a part of one item's blocks, of which the
+// warp takes every kAttnWarps-th step of two blocks.
+template <int RT>
+struct AttnSegment {
+  SeqWork sw;
+  int j0, take;     // the segment: blocks [j0, j0 + take) of the item
+  int head, r_first;
+  int blocks;       // of those, the ones that some row of the tile sees
+  int count;        // my steps
+
+  __device__ __forceinline__ AttnSegment(const AttnArgs& a, const AttnShare& s, int wt, int lane)
+      : b_(s.b), rem_(s.rem), left_(s.end - s.begin), wt_(wt), lane_(lane) {
+    sw = sequence_work<RT>(a, b_, false);
+  }
+
+  __device__ __forceinline__ void begin(const AttnArgs& a) {
+    while (rem_ >= sw.units) {  // the next sequence that has any work
+      rem_ = 0;
+      sw = sequence_work<RT>(a, ++b_, false);
+    }
+    const long long item = rem_ / sw.item_units;
+    const int at = static_cast<int>(rem_ - item * sw.item_units);
+    units_ = static_cast<int>(min(static_cast<long long>(sw.item_units - at), left_));
+    j0 = a.whole ? 0 : at;
+    take = a.whole ? sw.blocks : units_;
+    head = static_cast<int>(item / sw.tiles);
+    r_first = static_cast<int>(item % sw.tiles) * RT;
+    const int G = a.q_heads / a.kv_heads;
+    const int r_last = min(r_first + RT, sw.nq * G) - 1;
+    // tokens that the tile's last row sees, which no earlier row exceeds
+    const int reach = a.causal ? max(0, sw.len - sw.nq + r_last / G + 1) : sw.len;
+    blocks = max(0, min(take, (reach + kBlockTokens - 1) / kBlockTokens - j0));
+    const int steps = (blocks + 1) / 2;
+    count = steps > wt_ ? (steps - wt_ + kAttnWarps - 1) / kAttnWarps : 0;
+    look_up(a, 0, row_[0], sk_[0], sv_[0]);
+    look_up(a, 1, row_[1], sk_[1], sv_[1]);
+  }
+
+  // Whether there is another segment.
+  __device__ __forceinline__ bool advance() {
+    rem_ += units_;
+    left_ -= units_;
+    return left_ > 0;
+  }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && take == sw.blocks; }
+
+  // Row of the copy of step i, block lane % 2 (-1: none), while step `now` is looked at.
+  __device__ __forceinline__ int copy_row(int i, int now, int lane) const {
+    return __shfl_sync(0xFFFFFFFFu, (i >> 4) == (now >> 4) ? row_[0] : row_[1],
+                       2 * (i & 15) + (lane & 1));
+  }
+  __device__ __forceinline__ void scales(int i, int c, float& sk, float& sv) const {
+    sk = __shfl_sync(0xFFFFFFFFu, sk_[0], 2 * (i & 15) + c);
+    sv = __shfl_sync(0xFFFFFFFFu, sv_[0], 2 * (i & 15) + c);
+  }
+  // Step i is done.
+  __device__ __forceinline__ void next_blocks(int i, const AttnArgs& a) {
+    if ((i & 15) != 15) return;
+    row_[0] = row_[1];
+    sk_[0] = sk_[1];
+    sv_[0] = sv_[1];
+    look_up(a, (i >> 4) + 2, row_[1], sk_[1], sv_[1]);
+  }
+
+ private:
+  // Blocks of my steps 16 group .. + 15, one per lane: row of the copy, scales.
+  __device__ __forceinline__ void look_up(const AttnArgs& a, int group, int& row, float& sk,
+                                          float& sv) const {
+    const int i = 16 * group + (lane_ >> 1);
+    const int j = 2 * (wt_ + kAttnWarps * i) + (lane_ & 1);  // of the segment's blocks
+    row = -1;
+    sk = sv = 0.0f;
+    if (j >= blocks) return;
+    const int pos = (j0 + j) * kBlockTokens;
+    int page = a.table[static_cast<long long>(b_) * a.max_pages + pos / a.page_tokens];
+    if (page < 0 || page >= a.pages) {
+      raise_cache_error();
+      page = 0;
+    }
+    const long long hp = static_cast<long long>(page) * a.kv_heads + head;
+    const int slot = pos % a.page_tokens;
+    row = static_cast<int>(hp * a.page_tokens + slot);
+    const long long at = hp * (a.page_tokens / kBlockTokens) + slot / kBlockTokens;
+    sk = a.k_scale[at];
+    sv = a.v_scale[at];
+  }
+
+  int b_;
+  long long rem_, left_;  // the unit of sequence b_, units of the share
+  int wt_, lane_, units_;
+  int row_[2];            // this and the next sixteen steps' blocks, one per lane
+  float sk_[2], sv_[2];
+};
+
+// Copies of a step: lanes 0 and 1 fetch the keys and values of a block each (copy_row, -1
+// where there is none) into [keys 0, keys 1, values 0, values 1].
+template <int TILE>
+__device__ __forceinline__ void attn_copy(uint8_t* stage, const void* tm_k, const void* tm_v,
+                                          uint64_t* bar, int copy_row, int lane) {
+  const int other = __shfl_xor_sync(0xFFFFFFFFu, copy_row, 1);
+  if (lane == 0) mbar_arrive_expect_tx(bar, other >= 0 ? 4 * TILE : 2 * TILE);
+  __syncwarp();
+  if (lane < 2 && copy_row >= 0) {
+    tma_load_2d(stage + lane * TILE, tm_k, bar, 0, copy_row);
+    tma_load_2d(stage + (2 + lane) * TILE, tm_v, bar, 0, copy_row);
+  }
+}
+
+// Where the four of channels d .. d + 3 of a row lies in a warp's slab of sums, a whole stage
+// of its ring: rows of D floats, the fours of a row swizzled over the banks.
+template <int D>
+__device__ __forceinline__ int slab_offset(int row, int d) {
+  return row * D + (((d >> 2) ^ (row & 7)) << 2);
+}
+
+// The end of a segment: the warps' sums are joined relative to the largest maximum, in
+// order, and written as the result, or as a partial one where other CTAs have a part of the
+// item; rows [row0, row0 + ROWS) of a tile of RT.  In shared memory: row_m, row_l [warp][row]
+// maxima and sums of the warps' rows, slabs[warp] their outputs of these rows, already
+// relative to that maximum.
+template <int D, int RT, int ROWS>
 __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw,
-                                            const float (*row_m)[ROWS], const float (*row_l)[ROWS],
-                                            const float* const* slabs, int r_first, int head, bool whole,
-                                            bool from_start) {
-  constexpr int WT = kAttnWarps / WR, RT = ROWS * WR;
+                                            const float (*row_m)[RT], const float (*row_l)[RT],
+                                            const float* const* slabs, int r_first, int row0,
+                                            int head, bool whole, bool from_start) {
+  constexpr int WT = kAttnWarps;
   const int G = a.q_heads / a.kv_heads, rows = sw.nq * G;
   float* dst = a.partial + (static_cast<long long>(blockIdx.x) * 2 + (from_start ? 1 : 0)) *
                                (RT * (D + 2));
-  for (int i = threadIdx.x; i < RT * (D / 4); i += 32 * kAttnWarps) {
-    const int r = i / (D / 4), d = 4 * (i % (D / 4)), rw = r / ROWS, ri = r % ROWS;
+  for (int i = threadIdx.x; i < ROWS * (D / 4); i += 32 * kAttnWarps) {
+    const int r = row0 + i / (D / 4), d = 4 * (i % (D / 4));
     if (r_first + r >= rows) break;
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k * WR + rw][ri]);
+    for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k][r]);
     float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
     for (int k = 0; k < WT; ++k) {
-      const float mk = row_m[k * WR + rw][ri];
-      if (mk != -INFINITY) sum += row_l[k * WR + rw][ri] * exp2_approx(mk - top);
-      const float4 p = *reinterpret_cast<const float4*>(
-          slabs[k * WR + rw] + ri * (D + 4) + d);
+      const float mk = row_m[k][r];
+      if (mk != -INFINITY) sum += row_l[k][r] * exp2_approx(mk - top);
+      const float4 p = *reinterpret_cast<const float4*>(slabs[k] + slab_offset<D>(r - row0, d));
       v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
     }
     if (whole) {
@@ -384,139 +499,78 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
 }
 
 // One CTA of four warps takes an equal share of all units (so ragged batches stay
-// balanced and one long sequence fills the GPU), item by item.  WR warps cover the rows of
-// a tile, 16 MT each (with MT = 2 a code is made f16 once for 32 rows), the other factor
-// 4 / WR of the warps take steps of two blocks in turn.  Each such token group has its own
-// ring of steps, filled by bulk tensor copies that its first warp issues, so the warps run
-// independently between the ends of items.  Codes become f16 in registers, exactly; q
-// enters as f16 after a power-of-two scaling per row that keeps all its 8 bits; scores,
-// maxima, sums and the output are fp32.  Block scales multiply the scores (keys) and the
-// softmax weights relative to a power-of-two reference (values).
-template <int D, int MT, int WR>
+// balanced and one long sequence fills the GPU), item by item.  An item's steps of two blocks
+// are taken by the warps in turn, each with a ring of its own that bulk tensor copies fill, so
+// the warps run independently between the ends of segments; the first step of the next
+// segment is fetched while a segment's sums are joined.  Codes become f16 in registers,
+// exactly (with MT = 2 once for 32 query rows); q enters as f16 after a power-of-two scaling
+// per row that keeps all its 8 bits; scores, maxima, sums and the output are fp32.  Block
+// scales multiply the scores (keys) and the softmax weights relative to a power-of-two
+// reference (values).
+template <int D, int MT>
 struct AttnCfg {
-  static constexpr int WT = kAttnWarps / WR;   // token groups
-  static constexpr int ROWS = 16 * MT;         // of a warp
-  static constexpr int RT = ROWS * WR;         // of a tile
+  static constexpr int WT = kAttnWarps;
+  static constexpr int RT = 16 * MT;           // rows of a tile
   static constexpr int TILE = kBlockTokens * D;
   static constexpr int STEP = 4 * TILE;        // two blocks of keys and values
-  static constexpr int STAGES = D == 128 && WT == 4 ? 2 : 3;
+  static constexpr int STAGES = D == 128 ? 2 : 4;
   static constexpr bool QREG = MT * D <= 128;  // q stays in registers, else in shared memory
   static constexpr int RING = WT * STAGES * STEP;
-  static constexpr int SLABS = kAttnWarps * ROWS * (D + 4) * 4;  // over the ring
-  static constexpr int QBYTES = QREG ? 0 : kAttnWarps * ROWS * D * 2;
-  static constexpr int SMEM = (RING > SLABS ? RING : SLABS) + QBYTES + 1024;  // + alignment
-  static constexpr int CTAS = MT == 1 && D == 64 ? 3 : 2;                     // per SM
+  static constexpr int QBYTES = QREG ? 0 : WT * RT * D * 2;
+  static constexpr int SMEM = RING + QBYTES + 1024;  // + alignment
+  static constexpr int CTAS = MT == 1 && D == 64 ? 3 : 2;  // per SM
+  static_assert(16 * D * 4 <= STEP, "a warp's sums of sixteen rows fit one stage");
 };
 
-template <int D, int MT, int WR>
-__global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) attn_kv8_kernel(
+template <int D, int MT>
+__global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv8_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const AttnArgs a) {
-  using C = AttnCfg<D, MT, WR>;
-  constexpr int WT = C::WT, ROWS = C::ROWS, RT = C::RT, STAGES = C::STAGES, TILE = C::TILE;
-  constexpr int STEP = C::STEP;
+  using C = AttnCfg<D, MT>;
+  constexpr int WT = C::WT, RT = C::RT, STAGES = C::STAGES, TILE = C::TILE, STEP = C::STEP;
   constexpr bool QREG = C::QREG;
   constexpr int KS = D / 16;   // matrix steps over the channels
   constexpr int ND = D / 8;    // 8-channel tiles of the output
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* slabs = reinterpret_cast<float*>(ring);
-  __shared__ __align__(8) uint64_t full[WT][STAGES], empty[WT][STAGES];
-  __shared__ float row_m[kAttnWarps][ROWS], row_l[kAttnWarps][ROWS];
-  __shared__ const float* slab_at[kAttnWarps];
+  __shared__ __align__(8) uint64_t full[WT][STAGES];
+  __shared__ float row_m[WT][RT], row_l[WT][RT];
+  __shared__ const float* slab_at[WT];
   __shared__ AttnSched sched;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int wt = warp / WR, wr = warp % WR;
+  const int wt = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = a.q_heads / a.kv_heads;
   uint8_t* my_ring = ring + wt * STAGES * STEP;
   // [step over the channels][16-row half][lane] operands, a copy per warp
-  uint4* q_smem = reinterpret_cast<uint4*>(ring + (C::RING > C::SLABS ? C::RING : C::SLABS)) +
-                  warp * (QREG ? 0 : KS * MT * 32) + lane;
+  uint4* q_smem = reinterpret_cast<uint4*>(ring + C::RING) + wt * (QREG ? 0 : KS * MT * 32) + lane;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < WT; ++i)
-      for (int s = 0; s < STAGES; ++s) {
-        mbar_init(&full[i][s], 1);
-        mbar_init(&empty[i][s], WR);
-      }
+      for (int s = 0; s < STAGES; ++s) mbar_init(&full[i][s], 1);
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (lane == 0) slab_at[warp] = slabs + warp * ROWS * (D + 4);
   griddep_wait();
   griddep_launch_dependents();
   const AttnShare share = attn_share<RT>(a, sched);
   if (share.begin >= share.end) return;
 
-  int b = share.b;
-  long long rem = share.rem;
-  uint32_t phase = 0;  // steps this token group has taken so far (stage and parity)
-  SeqWork sw = sequence_work<RT>(a, b, false);
-  for (long long u = share.begin; u < share.end;) {
-    while (rem >= sw.units) {  // the next sequence that has any work
-      rem = 0;
-      sw = sequence_work<RT>(a, ++b, false);
-    }
-    const long long item = rem / sw.item_units;
-    const int at = static_cast<int>(rem - item * sw.item_units);
-    const int units = static_cast<int>(min(static_cast<long long>(sw.item_units - at), share.end - u));
-    const int j0 = a.whole ? 0 : at, take = a.whole ? sw.blocks : units;
-    const int head = static_cast<int>(item / sw.tiles), tile = static_cast<int>(item % sw.tiles);
+  uint32_t phase = 0;  // steps this warp has taken before this segment (stage and parity)
+  AttnSegment<RT> seg(a, share, wt, lane);
+  auto issue = [&](int i, int consumed) {  // copies of my step i: two lanes, a block each
+    const int copy_row = seg.copy_row(i, consumed, lane);
+    const uint32_t st = (phase + i) % STAGES;
+    attn_copy<TILE>(my_ring + st * STEP, &tm_k, &tm_v, &full[wt][st], copy_row, lane);
+  };
+  seg.begin(a);
+  if (seg.count > 0) issue(0, 0);
+
+  for (;;) {
+    const int count = seg.count, j0 = seg.j0, blocks = seg.blocks, head = seg.head, r_first = seg.r_first;
+    const SeqWork sw = seg.sw;
     const int rows = sw.nq * G;
-    const int r_first = tile * RT, r_last = min(r_first + RT, rows) - 1;
-    // tokens that the tile's last row sees, which no earlier row exceeds
-    const int reach = a.causal ? max(0, sw.len - sw.nq + r_last / G + 1) : sw.len;
-    const int blocks = max(0, min(take, (reach + kBlockTokens - 1) / kBlockTokens - j0));
-    const int steps = (blocks + 1) / 2;
-    const int count = steps > wt ? (steps - wt + WT - 1) / WT : 0;  // my steps
-
-    // my upcoming blocks, one per lane (two to a step): row of the copy (-1: none), scales
-    const int page_blocks = a.page_tokens / kBlockTokens;
-    auto look_up = [&](int group, int& copy_row, float& sk, float& sv) {
-      const int i = 16 * group + (lane >> 1);
-      const int j = 2 * (wt + WT * i) + (lane & 1);  // of the segment's blocks
-      copy_row = -1;
-      sk = sv = 0.0f;
-      if (j >= blocks) return;
-      const int pos = (j0 + j) * kBlockTokens;
-      int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
-      if (page < 0 || page >= a.pages) {
-        raise_cache_error();
-        page = 0;
-      }
-      const long long hp = static_cast<long long>(page) * a.kv_heads + head;
-      const int slot = pos % a.page_tokens;
-      copy_row = static_cast<int>(hp * a.page_tokens + slot);
-      sk = a.k_scale[hp * page_blocks + slot / kBlockTokens];
-      sv = a.v_scale[hp * page_blocks + slot / kBlockTokens];
-    };
-    int row_a, row_b;
-    float sk_a, sv_a, sk_b, sv_b;
-    look_up(0, row_a, sk_a, sv_a);
-    look_up(1, row_b, sk_b, sv_b);
-
-    auto issue = [&](int i, int consumed) {  // copies of my step i: two lanes, a block each
-      const bool cur = (i >> 4) == (consumed >> 4);
-      const int copy_row = __shfl_sync(0xFFFFFFFFu, cur ? row_a : row_b, 2 * (i & 15) + (lane & 1));
-      const int other = __shfl_xor_sync(0xFFFFFFFFu, copy_row, 1);
-      if (wr == 0) {
-        const uint32_t n = phase + i, st = n % STAGES, round = n / STAGES;
-        bool ok = true;
-        if (WR > 1 && round > 0) ok = mbar_wait_drain(&empty[wt][st], (round - 1) & 1);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (lane == 0 && ok) mbar_arrive_expect_tx(&full[wt][st], other >= 0 ? 4 * TILE : 2 * TILE);
-        __syncwarp();
-        if (lane < 2 && ok && copy_row >= 0) {
-          uint8_t* dst = my_ring + st * STEP + lane * TILE;
-          tma_load_2d(dst, &tm_k, &full[wt][st], 0, copy_row);
-          tma_load_2d(dst + 2 * TILE, &tm_v, &full[wt][st], 0, copy_row);
-        }
-      }
-      __syncwarp();
-    };
-    int issued = 0;
+    int issued = min(count, 1);
     for (; issued < min(count, STAGES); ++issued) issue(issued, 0);
 
     // my rows: g and g + 8 of each sixteen.  q as f16 operands: channel 32t + 16x + 4w + 0..3
@@ -531,7 +585,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
       uint32_t f[KS][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = r_first + ROWS * wr + 16 * mt + 8 * h + g;
+        const int r = r_first + 16 * mt + 8 * h + g;
         const bool valid = r < rows;
         const int qi = valid ? r / G : 0, qh = head * G + (valid ? r % G : 0);
         see[mt][h] = valid && a.causal ? sw.len - sw.nq + qi + 1 : sw.len;
@@ -587,9 +641,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
       }
     float ref = 0.0f, inv_ref = 0.0f;  // power of two >= the value scales seen
     int dead = -1;  // the step whose copies did not arrive in time
-    // a stage is refilled when its readers are done: at once where there is one reader, one
-    // step later where several warps share it, so that none waits for the slowest
-    constexpr int LAG = WR > 1 ? 1 : 0;
     for (int i = 0; i < count; ++i) {
       const uint32_t n = phase + i, st = n % STAGES;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_drain(&full[wt][st], (n / STAGES) & 1))) {
@@ -635,10 +686,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
 
       float sk[2], sv[2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        sk[c] = __shfl_sync(0xFFFFFFFFu, sk_a, 2 * (i & 15) + c);
-        sv[c] = __shfl_sync(0xFFFFFFFFu, sv_a, 2 * (i & 15) + c);
-      }
+      for (int c = 0; c < 2; ++c) seg.scales(i, c, sk[c], sv[c]);
       const int first = (j0 + 2 * (wt + WT * i)) * kBlockTokens;
       const int last = (j0 + blocks) * kBlockTokens;
       const bool cut = first + 2 * kBlockTokens > min(see_min, last);
@@ -753,22 +801,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
         }
       }
       __syncwarp();  // the stage has been read
-      if (WR > 1 && lane == 0) mbar_arrive(&empty[wt][st]);
-      if (issued < count && issued < i + 1 + STAGES - LAG) {
+      if (issued < count) {
         issue(issued, i);
         ++issued;
       }
-      if ((i & 15) == 15) {
-        row_a = row_b; sk_a = sk_b; sv_a = sv_b;
-        look_up((i >> 4) + 2, row_b, sk_b, sv_b);
-      }
+      seg.next_blocks(i, a);
     }
-    if (dead >= 0 && wr == 0 && lane == 0)  // wait (bounded) for the copies in flight
+    if (dead >= 0 && lane == 0)  // wait (bounded) for the copies in flight
       for (int i = dead; i < issued; ++i)
         mbar_wait_drain(&full[wt][(phase + i) % STAGES], ((phase + i) / STAGES) & 1);
     phase += count;
 
-    // join the token groups
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -776,37 +819,49 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT, WR>::CTAS) att
         l[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][h], 1);
         l[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][h], 2);
         if (t == 0) {
-          row_m[warp][16 * mt + 8 * h + g] = m[mt][h];
-          row_l[warp][16 * mt + 8 * h + g] = l[mt][h];
+          row_m[wt][16 * mt + 8 * h + g] = m[mt][h];
+          row_l[wt][16 * mt + 8 * h + g] = l[mt][h];
         }
       }
-    __syncthreads();  // also: every ring is drained, the slabs may lie over them
+    // on to the next segment: its first copies go to the stage `phase` names, this one's sums
+    // to the others of the warp's own ring, whose stages have all been read
+    const bool whole = seg.whole(), from_start = j0 == 0;
+    const bool more = seg.advance() && __all_sync(0xFFFFFFFFu, dead < 0);
+    float* slab = reinterpret_cast<float*>(my_ring + (phase + 1) % STAGES * STEP);
+    if (lane == 0) slab_at[wt] = slab;
+    if (more) {
+      seg.begin(a);
+      if (seg.count > 0) issue(0, 0);
+    }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      __syncthreads();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = 16 * mt + 8 * h + g;
+        const int row = 8 * h + g;
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < WT; ++i) top = fmaxf(top, row_m[i * WR + wr][row]);
-        const float f = m[mt][h] == -INFINITY ? 0.0f : exp2_approx(m[mt][h] - top) * ref;
-        float* dst = slabs + (warp * ROWS + row) * (D + 4) + t * (D / 4);
+        for (int i = 0; i < WT; ++i) top = fmaxf(top, row_m[i][16 * mt + row]);
+        const float fade = m[mt][h] == -INFINITY ? 0.0f : exp2_approx(m[mt][h] - top) * ref;
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int nd = 0; nd < ND; nd += 4)
-            *reinterpret_cast<float4*>(dst + part * ND + nd) = make_float4(
-                o[mt][nd][2 * h + part] * f, o[mt][nd + 1][2 * h + part] * f,
-                o[mt][nd + 2][2 * h + part] * f, o[mt][nd + 3][2 * h + part] * f);
+            *reinterpret_cast<float4*>(slab + slab_offset<D>(row, t * (D / 4) + part * ND + nd)) =
+                make_float4(o[mt][nd][2 * h + part] * fade, o[mt][nd + 1][2 * h + part] * fade,
+                            o[mt][nd + 2][2 * h + part] * fade, o[mt][nd + 3][2 * h + part] * fade);
       }
-    __syncthreads();
-    attn_finish<D, WR, ROWS>(a, sw, row_m, row_l, slab_at, r_first, head,
-                             j0 == 0 && take == sw.blocks, j0 == 0);
-    // the next copies write where the slabs were read and written by ordinary accesses
+      __syncthreads();
+      attn_finish<D, RT, 16>(a, sw, row_m, row_l, slab_at, r_first, 16 * mt, head, whole, from_start);
+    }
+    // the next copies write where the sums were written and read by ordinary accesses
     fence_proxy_async_smem();
-    if (__syncthreads_or(dead >= 0)) return;  // the error word is set
-    u += units;
-    rem += units;
+    if (__syncthreads_or(dead >= 0)) {  // the error word is set
+      if (more && seg.count > 0 && lane == 0)
+        mbar_wait_drain(&full[wt][phase % STAGES], (phase / STAGES) & 1);
+      return;
+    }
+    if (!more) return;
   }
 }
 
@@ -832,7 +887,7 @@ struct AttnFewCfg {
   static constexpr int RING = WT * STAGES * STEP;
   static constexpr int SMEM = RING + 1024;            // + alignment
   static constexpr int CTAS = D == 128 ? 3 : 4;
-  static_assert(RT * (D + 4) * 4 <= STEP, "a warp's sums fit one stage");
+  static_assert(RT * D * 4 <= STEP, "a warp's sums fit one stage");
 };
 
 template <int D, int RT_>
@@ -867,72 +922,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
   const AttnShare share = attn_share<RT>(a, sched);
   if (share.begin >= share.end) return;
 
-  int b = share.b;
-  long long rem = share.rem, u = share.begin;
   uint32_t phase = 0;  // steps this warp has taken before this segment (stage and parity)
-  SeqWork sw = sequence_work<RT>(a, b, false);
-
-  // The segment at (b, rem): part of an item's blocks
-  int units, j0, take, head, r_first, blocks, count;
-  int row_a, row_b;  // my upcoming blocks, one per lane (two to a step): row of the copy (-1: none),
-  float sk_a, sv_a, sk_b, sv_b;  // and scales; now and next
-  const int page_blocks = a.page_tokens / kBlockTokens;
-  auto look_up = [&](int group, int& copy_row, float& sk, float& sv) {
-    const int i = 16 * group + (lane >> 1);
-    const int j = 2 * (wt + WT * i) + (lane & 1);  // of the segment's blocks
-    copy_row = -1;
-    sk = sv = 0.0f;
-    if (j >= blocks) return;
-    const int pos = (j0 + j) * kBlockTokens;
-    int page = a.table[static_cast<long long>(b) * a.max_pages + pos / a.page_tokens];
-    if (page < 0 || page >= a.pages) {
-      raise_cache_error();
-      page = 0;
-    }
-    const long long hp = static_cast<long long>(page) * a.kv_heads + head;
-    const int slot = pos % a.page_tokens;
-    copy_row = static_cast<int>(hp * a.page_tokens + slot);
-    sk = a.k_scale[hp * page_blocks + slot / kBlockTokens];
-    sv = a.v_scale[hp * page_blocks + slot / kBlockTokens];
-  };
+  AttnSegment<RT> seg(a, share, wt, lane);
   auto issue = [&](int i, int consumed) {  // copies of my step i: two lanes, a block each
-    const bool cur = (i >> 4) == (consumed >> 4);
-    const int copy_row = __shfl_sync(0xFFFFFFFFu, cur ? row_a : row_b, 2 * (i & 15) + (lane & 1));
-    const int other = __shfl_xor_sync(0xFFFFFFFFu, copy_row, 1);
+    const int copy_row = seg.copy_row(i, consumed, lane);
     const uint32_t st = (phase + i) % STAGES;
-    if (lane == 0) mbar_arrive_expect_tx(&full[wt][st], other >= 0 ? 4 * TILE : 2 * TILE);
-    __syncwarp();
-    if (lane < 2 && copy_row >= 0) {
-      uint8_t* dst = my_ring + st * STEP + lane * TILE;
-      tma_load_2d(dst, &tm_k, &full[wt][st], 0, copy_row);
-      tma_load_2d(dst + 2 * TILE, &tm_v, &full[wt][st], 0, copy_row);
-    }
+    attn_copy<TILE>(my_ring + st * STEP, &tm_k, &tm_v, &full[wt][st], copy_row, lane);
   };
-  auto begin_segment = [&]() {
-    while (rem >= sw.units) {  // the next sequence that has any work
-      rem = 0;
-      sw = sequence_work<RT>(a, ++b, false);
-    }
-    const long long item = rem / sw.item_units;
-    const int at = static_cast<int>(rem - item * sw.item_units);
-    units = static_cast<int>(min(static_cast<long long>(sw.item_units - at), share.end - u));
-    j0 = a.whole ? 0 : at;
-    take = a.whole ? sw.blocks : units;
-    head = static_cast<int>(item / sw.tiles);
-    r_first = static_cast<int>(item % sw.tiles) * RT;
-    const int r_last = min(r_first + RT, sw.nq * G) - 1;
-    // tokens that the tile's last row sees, which no earlier row exceeds
-    const int reach = a.causal ? max(0, sw.len - sw.nq + r_last / G + 1) : sw.len;
-    blocks = max(0, min(take, (reach + kBlockTokens - 1) / kBlockTokens - j0));
-    const int steps = (blocks + 1) / 2;
-    count = steps > wt ? (steps - wt + WT - 1) / WT : 0;  // my steps
-    look_up(0, row_a, sk_a, sv_a);
-    look_up(1, row_b, sk_b, sv_b);
-    if (count > 0) issue(0, 0);
-  };
-  begin_segment();
+  seg.begin(a);
+  if (seg.count > 0) issue(0, 0);
 
   for (;;) {
+    const int count = seg.count, j0 = seg.j0, blocks = seg.blocks, head = seg.head, r_first = seg.r_first;
+    const SeqWork sw = seg.sw;
     int issued = min(count, 1);
     for (; issued < min(count, STAGES); ++issued) issue(issued, 0);
 
@@ -1007,8 +1009,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
       float s[2][2][2];   // [block][tile of 8 tokens][token 2t, 2t + 1]
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        f[c] = qs * __shfl_sync(0xFFFFFFFFu, sk_a, 2 * (i & 15) + c);
-        sv[c] = __shfl_sync(0xFFFFFFFFu, sv_a, 2 * (i & 15) + c);
+        float sk;
+        seg.scales(i, c, sk, sv[c]);
+        f[c] = qs * sk;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           int hm[4], lo[4];
@@ -1117,10 +1120,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
         issue(issued, i);
         ++issued;
       }
-      if ((i & 15) == 15) {
-        row_a = row_b; sk_a = sk_b; sv_a = sv_b;
-        look_up((i >> 4) + 2, row_b, sk_b, sv_b);
-      }
+      seg.next_blocks(i, a);
     }
     if (dead >= 0 && lane == 0)  // wait (bounded) for the copies in flight
       for (int i = dead; i < issued; ++i)
@@ -1135,14 +1135,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
     }
     // on to the next segment: its first copies go to the stage `phase` names, this one's
     // sums to the other (of the warp's own ring, whose stages have all been read)
-    const SeqWork sw_now = sw;
-    const int head_now = head, r_now = r_first;
-    const bool whole = j0 == 0 && take == sw.blocks, from_start = j0 == 0;
-    u += units;
-    rem += units;
-    const bool more = u < share.end && __all_sync(0xFFFFFFFFu, dead < 0);
+    const bool whole = seg.whole(), from_start = j0 == 0;
+    const bool more = seg.advance() && __all_sync(0xFFFFFFFFu, dead < 0);
     float* slab = reinterpret_cast<float*>(my_ring + (phase + 1) % STAGES * STEP);
-    if (more) begin_segment();
+    if (more) {
+      seg.begin(a);
+      if (seg.count > 0) issue(0, 0);
+    }
     __syncthreads();
     float top = -INFINITY;
 #pragma unroll
@@ -1152,19 +1151,18 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (2 * t + e >= RT) break;
-      float* dst = slab + (2 * t + e) * (D + 4) + g * (D / 8);
 #pragma unroll
       for (int x = 0; x < MD; x += 2)
-        *reinterpret_cast<float4*>(dst + 2 * x) =
+        *reinterpret_cast<float4*>(slab + slab_offset<D>(2 * t + e, g * (D / 8) + 2 * x)) =
             make_float4(o[x][e] * fq[e], o[x][2 + e] * fq[e], o[x + 1][e] * fq[e], o[x + 1][2 + e] * fq[e]);
     }
     if (lane == 0) slab_at[wt] = slab;
     __syncthreads();
-    attn_finish<D, 1, RT>(a, sw_now, row_m, row_l, slab_at, r_now, head_now, whole, from_start);
+    attn_finish<D, RT, RT>(a, sw, row_m, row_l, slab_at, r_first, 0, head, whole, from_start);
     // the next copies write where the sums were written and read by ordinary accesses
     fence_proxy_async_smem();
     if (__syncthreads_or(dead >= 0)) {  // the error word is set
-      if (more && count > 0 && lane == 0)
+      if (more && seg.count > 0 && lane == 0)
         mbar_wait_drain(&full[wt][phase % STAGES], (phase / STAGES) & 1);
       return;
     }
@@ -1261,10 +1259,11 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
 // ------------------------------------------------------------ host side
 
 // Rows of a tile, by the rows per cache head that an average sequence has: 4 or 8 (their
-// own kernel), 16 or 32 (one warp wide), or 64 (two warps of 32 side by side).
+// own kernel), 16 or 32.  (64 rows on pairs of warps that shared their copies lost to two
+// tiles of 32 everywhere: 57.9 / 54.4 us for chunks of 64 over 8512 tokens, heads of 64.)
 int attn_tile_rows(int Tq, int B, int q_heads, int kv_heads) {
   const long long rows = static_cast<long long>(Tq) * (q_heads / kv_heads);
-  return rows <= 4LL * B ? 4 : rows <= 8LL * B ? 8 : rows <= 16LL * B ? 16 : rows <= 32LL * B ? 32 : 64;
+  return rows <= 4LL * B ? 4 : rows <= 8LL * B ? 8 : rows <= 16LL * B ? 16 : 32;
 }
 
 // Whether items are left whole, one CTA each, and the joining kernel is not launched: where
@@ -1311,19 +1310,17 @@ cudaError_t run_attn(Kernel kernel, std::atomic<bool> (&done)[kAttrDevices], int
 template <int D>
 cudaError_t dispatch_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a,
                           int RT, cudaStream_t st) {
-  static std::atomic<bool> done[5][kAttrDevices];
+  static std::atomic<bool> done[4][kAttrDevices];
 #define WQ_ATTN(I_, CFG_, KERNEL_) \
   return run_attn(KERNEL_, done[I_], CFG_::SMEM, CFG_::CTAS, tm_k, tm_v, a, D, RT, st)
-  using C16 = AttnCfg<D, 1, 1>;
-  using C32 = AttnCfg<D, 2, 1>;
-  using C64 = AttnCfg<D, 2, 2>;
+  using C16 = AttnCfg<D, 1>;
+  using C32 = AttnCfg<D, 2>;
   using C4 = AttnFewCfg<D, 4>;
   using C8 = AttnFewCfg<D, 8>;
-  if (RT == 4) WQ_ATTN(4, C4, (attn_kv8_few_kernel<D, 4>));
-  if (RT == 8) WQ_ATTN(0, C8, (attn_kv8_few_kernel<D, 8>));
-  if (RT == 16) WQ_ATTN(1, C16, (attn_kv8_kernel<D, 1, 1>));
-  if (RT == 32) WQ_ATTN(2, C32, (attn_kv8_kernel<D, 2, 1>));
-  WQ_ATTN(3, C64, (attn_kv8_kernel<D, 2, 2>));
+  if (RT == 4) WQ_ATTN(0, C4, (attn_kv8_few_kernel<D, 4>));
+  if (RT == 8) WQ_ATTN(1, C8, (attn_kv8_few_kernel<D, 8>));
+  if (RT == 16) WQ_ATTN(2, C16, (attn_kv8_kernel<D, 1>));
+  WQ_ATTN(3, C32, (attn_kv8_kernel<D, 2>));
 #undef WQ_ATTN
 }
 
