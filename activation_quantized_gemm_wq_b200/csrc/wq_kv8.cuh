@@ -234,11 +234,21 @@ struct AttnArgs {
   const float* v_scale;
   uint16_t* out;          // bf16 [Tq][q_heads][D]
   float* lse;             // [Tq][q_heads] or null
-  long long* prefix;      // workspace: [B + 1] units before each sequence
+  struct AttnCut* cuts;   // workspace: [grid], what each CTA's end cuts
   float* partial;         // workspace: [grid][2] partial results
   int Tq, B, q_heads, kv_heads, max_pages, pages, page_tokens, causal;
   int whole;              // items are not cut: a unit is an item
   float scale_log2;       // softmax scale * log2(e)
+};
+
+// The item that a CTA's end cuts: parts of it lie at CTA c0, as its second partial result,
+// and at c0 + 1 .. c0 + ends, as their first.
+struct __align__(16) AttnCut {
+  int ends;           // ends of CTAs inside the item; 0: this CTA's end cuts none
+  int c0;
+  int q0, head;       // the sequence's first query row, the item's cache head
+  int r_first, rows;  // the tile's rows
+  int unused[2];
 };
 
 // What a sequence asks for: the work is cut into units of one block of 16 tokens for one
@@ -277,10 +287,10 @@ __device__ __forceinline__ long long units_per_cta(long long total, int grid, in
 
 // Units before every sequence: each thread sums a run of them, then a scan over threads.
 // Every CTA finds its share [begin, end) of them and where that starts: sequence b, unit
-// rem of it; CTA 0 leaves the sums for the joining kernel.
+// rem of it.
 struct AttnSched {
   long long scan[kAttnWarps];
-  long long rem;
+  long long rem, end, per;
   int b;
 };
 
@@ -316,18 +326,20 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, AttnSched& sh
   const long long per = units_per_cta(total, gridDim.x, a.whole);
   s.begin = min(per * blockIdx.x, total);
   s.end = min(s.begin + per, total);
-  if (blockIdx.x == 0 || (s.begin >= before && s.begin < before + mine)) {
+  if (threadIdx.x == 0) {
+    sh.end = s.end;
+    sh.per = per;
+  }
+  if (s.begin >= before && s.begin < before + mine) {
     long long at = before;
     for (int b = b_lo; b < b_hi; ++b) {
       const long long n = sequence_work<RT>(a, b, false).units;
-      if (blockIdx.x == 0) a.prefix[b] = at;
       if (s.begin >= at && s.begin < at + n) {
         sh.b = b;
         sh.rem = s.begin - at;
       }
       at += n;
     }
-    if (blockIdx.x == 0 && b_hi == a.B && b_lo < b_hi) a.prefix[a.B] = at;
   }
   __syncthreads();
   s.b = sh.b;
@@ -373,8 +385,22 @@ struct AttnSegment {
     look_up(a, 1, row_[1], sk_[1], sv_[1]);
   }
 
-  // Whether there is another segment.
-  __device__ __forceinline__ bool advance() {
+  // Whether there is another segment; behind the last one, what the CTA's end cuts.
+  __device__ __forceinline__ bool advance(const AttnArgs& a, const AttnSched& sh) {
+    if (left_ == units_ && threadIdx.x == 0) {
+      AttnCut c;
+      c.ends = c.c0 = 0;
+      if (!a.whole && j0 + take < sw.blocks) {
+        const long long u0 = sh.end - units_ - j0;  // the item's first unit
+        c.c0 = static_cast<int>(u0 / sh.per);
+        c.ends = static_cast<int>((u0 + sw.blocks - 1) / sh.per) - c.c0;
+      }
+      c.q0 = sw.q0;
+      c.head = head;
+      c.r_first = r_first;
+      c.rows = min(RT, sw.nq * (a.q_heads / a.kv_heads) - r_first);
+      a.cuts[blockIdx.x] = c;
+    }
     rem_ += units_;
     left_ -= units_;
     return left_ > 0;
@@ -423,7 +449,7 @@ struct AttnSegment {
   }
 
   int b_;
-  long long rem_, left_;  // the unit of sequence b_, units of the share
+  long long rem_, left_;  // the unit of sequence b_, units left of the share
   int wt_, lane_, units_;
   int row_[2];            // this and the next sixteen steps' blocks, one per lane
   float sk_[2], sv_[2];
@@ -554,7 +580,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
   griddep_wait();
   griddep_launch_dependents();
   const AttnShare share = attn_share<RT>(a, sched);
-  if (share.begin >= share.end) return;
+  if (share.begin >= share.end) {
+    if (threadIdx.x == 0) a.cuts[blockIdx.x].ends = 0;
+    return;
+  }
 
   uint32_t phase = 0;  // steps this warp has taken before this segment (stage and parity)
   AttnSegment<RT> seg(a, share, wt, lane);
@@ -826,7 +855,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
     // on to the next segment: its first copies go to the stage `phase` names, this one's sums
     // to the others of the warp's own ring, whose stages have all been read
     const bool whole = seg.whole(), from_start = j0 == 0;
-    const bool more = seg.advance() && __all_sync(0xFFFFFFFFu, dead < 0);
+    const bool more = seg.advance(a, sched) && __all_sync(0xFFFFFFFFu, dead < 0);
     float* slab = reinterpret_cast<float*>(my_ring + (phase + 1) % STAGES * STEP);
     if (lane == 0) slab_at[wt] = slab;
     if (more) {
@@ -920,7 +949,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
   griddep_wait();
   griddep_launch_dependents();
   const AttnShare share = attn_share<RT>(a, sched);
-  if (share.begin >= share.end) return;
+  if (share.begin >= share.end) {
+    if (threadIdx.x == 0) a.cuts[blockIdx.x].ends = 0;
+    return;
+  }
 
   uint32_t phase = 0;  // steps this warp has taken before this segment (stage and parity)
   AttnSegment<RT> seg(a, share, wt, lane);
@@ -1136,7 +1168,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
     // on to the next segment: its first copies go to the stage `phase` names, this one's
     // sums to the other (of the warp's own ring, whose stages have all been read)
     const bool whole = seg.whole(), from_start = j0 == 0;
-    const bool more = seg.advance() && __all_sync(0xFFFFFFFFu, dead < 0);
+    const bool more = seg.advance(a, sched) && __all_sync(0xFFFFFFFFu, dead < 0);
     float* slab = reinterpret_cast<float*>(my_ring + (phase + 1) % STAGES * STEP);
     if (more) {
       seg.begin(a);
@@ -1178,39 +1210,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
 constexpr int kJoinSplit = 4;
 
 template <int D>
-__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, int grid, int RT) {
+__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, int RT) {
   griddep_wait();
   griddep_launch_dependents();
-  const long long total = a.prefix[a.B];
-  const long long per = units_per_cta(total, grid, 0);
-  const long long cut = per * (blockIdx.x / kJoinSplit + 1);
-  if (cut >= total) return;
-  // the sequence that unit `cut` belongs to: the last b with prefix[b] <= cut
   const int lane = threadIdx.x & 31;
-  int b = 0;
-  for (int span = a.B; span > 1;) {
-    const int step = (span + 31) / 32;
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, lane * step < span && a.prefix[b + (lane * step < span ? lane * step : 0)] <= cut);
-    const int k = hit ? 31 - __clz(hit) : 0;
-    span = min(step, span - k * step);
-    b += k * step;
-  }
+  const AttnCut cut = a.cuts[blockIdx.x / kJoinSplit];
+  if (cut.ends == 0) return;
   const int G = a.q_heads / a.kv_heads;
-  const int q0 = min(max(a.q_start[b], 0), a.Tq), nq = max(min(a.q_start[b + 1], a.Tq) - q0, 0);
-  const long long before = a.prefix[b], units = a.prefix[b + 1] - before;
-  const int tiles = static_cast<int>((static_cast<long long>(nq) * G + RT - 1) / RT);
-  if (tiles == 0) return;
-  const long long blocks = units / (static_cast<long long>(tiles) * a.kv_heads);
-  const long long item = (cut - before) / blocks, u0 = before + item * blocks;
-  if (u0 == cut) return;  // a CTA ends where an item does
-  const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + blocks - 1) / per);
-  const int head = static_cast<int>(item / tiles), r_first = static_cast<int>(item % tiles) * RT;
-  const int rows = min(RT, nq * G - r_first);
+  const int c0 = cut.c0, c1 = c0 + cut.ends;
   const long long size = static_cast<long long>(RT) * (D + 2);
   int lanes = 2;  // to an output
   while (lanes < 32 && lanes <= c1 - c0) lanes *= 2;
   // my piece of the outputs, in fours
-  const int all = rows * (D / 4), pieces = (c1 - c0) * kJoinSplit;
+  const int all = cut.rows * (D / 4), pieces = cut.ends * kJoinSplit;
   const int my = blockIdx.x - c0 * kJoinSplit, end = all * (my + 1) / pieces;
   for (int base = all * my / pieces; base < end; base += 128 / lanes) {
     const int i = min(base + static_cast<int>(threadIdx.x) / lanes, end - 1);
@@ -1218,7 +1230,7 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
     float top = -INFINITY, sum = 0.0f;
     float4 v = make_float4(0, 0, 0, 0);
     for (int c = c0 + lane % lanes; c <= c1; c += lanes) {
-      const float* p = a.partial + (2LL * c + (static_cast<long long>(c) * per > u0 ? 0 : 1)) * size;
+      const float* p = a.partial + (2LL * c + (c == c0 ? 1 : 0)) * size;
       const float2 ml = *reinterpret_cast<const float2*>(p + RT * D + 2 * r);
       const float4 x = *reinterpret_cast<const float4*>(p + r * D + d);
       const float to = fmaxf(top, ml.x);
@@ -1245,8 +1257,8 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
     }
     if (lane % lanes != 0 || base + static_cast<int>(threadIdx.x) / lanes >= end) continue;
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const int qi = (r_first + r) / G, qh = head * G + (r_first + r) % G;
-    const long long at = static_cast<long long>(q0 + qi) * a.q_heads + qh;
+    const int qi = (cut.r_first + r) / G, qh = cut.head * G + (cut.r_first + r) % G;
+    const long long at = static_cast<long long>(cut.q0 + qi) * a.q_heads + qh;
     const __nv_bfloat162 x0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
     const __nv_bfloat162 x1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
     *reinterpret_cast<uint2*>(a.out + at * D + d) =
@@ -1279,7 +1291,7 @@ bool attn_whole(const Kv8Cache& c, int Tq, int q_heads, int RT) {
 
 constexpr int kAttnMaxCtas = 4;  // per SM, of any instance
 
-size_t attn_prefix_bytes(int B) { return (8 * (static_cast<size_t>(B) + 1) + 255) / 256 * 256; }
+size_t attn_cut_bytes(size_t grid) { return (grid * sizeof(AttnCut) + 255) / 256 * 256; }
 
 bool cache_map(CUtensorMap* m, const void* base, int D, long long rows) {
   EncodeTiledFn fn = encode_fn();
@@ -1304,7 +1316,7 @@ cudaError_t run_attn(Kernel kernel, std::atomic<bool> (&done)[kAttrDevices], int
   const cudaError_t f = launch_pdl(kernel, grid, 32 * kAttnWarps, smem, st, 1, tm_k, tm_v, a);
   if (f != cudaSuccess || a.whole) return f;
   return launch_pdl(D == 128 ? attn_kv8_join_kernel<128> : attn_kv8_join_kernel<64>,
-                    (grid - 1) * kJoinSplit, 128, 0, st, 1, a, grid, RT);
+                    (grid - 1) * kJoinSplit, 128, 0, st, 1, a, RT);
 }
 
 template <int D>
@@ -1346,7 +1358,7 @@ cudaError_t launch_kv8_append(const Kv8Append& p, cudaStream_t st) {
 size_t attn_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int D) {
   const size_t rt = attn_tile_rows(Tq, B, q_heads, kv_heads);
   const size_t grid = static_cast<size_t>(sm_count()) * kAttnMaxCtas;
-  return attn_prefix_bytes(B) + (grid * 2 * rt * (D + 2) * 4 + 255) / 256 * 256;
+  return attn_cut_bytes(grid) + (grid * 2 * rt * (D + 2) * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_attn_kv8(const Kv8Attn& p, cudaStream_t st) {
@@ -1359,8 +1371,9 @@ cudaError_t launch_attn_kv8(const Kv8Attn& p, cudaStream_t st) {
   a.q = p.q; a.q_stride = p.q_stride; a.q_start = p.q_start; a.kv_len = p.kv_len;
   a.table = p.cache.table; a.k_scale = p.cache.k_scale; a.v_scale = p.cache.v_scale;
   a.out = p.out; a.lse = p.lse;
-  a.prefix = static_cast<long long*>(p.workspace);
-  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + attn_prefix_bytes(p.cache.B));
+  a.cuts = static_cast<AttnCut*>(p.workspace);
+  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) +
+                                       attn_cut_bytes(static_cast<size_t>(sm_count()) * kAttnMaxCtas));
   a.Tq = p.Tq; a.B = p.cache.B; a.q_heads = p.q_heads; a.kv_heads = p.cache.kv_heads;
   a.max_pages = p.cache.max_pages; a.pages = p.cache.pages; a.page_tokens = p.cache.page_tokens;
   a.causal = p.causal; a.scale_log2 = p.scale * 1.4426950408889634f;
