@@ -329,6 +329,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, AttnSched& sh
   if (threadIdx.x == 0) {
     sh.end = s.end;
     sh.per = per;
+    a.cuts[blockIdx.x].ends = 0;  // until the last segment says otherwise
   }
   if (s.begin >= before && s.begin < before + mine) {
     long long at = before;
@@ -387,14 +388,11 @@ struct AttnSegment {
 
   // Whether there is another segment; behind the last one, what the CTA's end cuts.
   __device__ __forceinline__ bool advance(const AttnArgs& a, const AttnSched& sh) {
-    if (left_ == units_ && threadIdx.x == 0) {
+    if (left_ == units_ && threadIdx.x == 0 && !a.whole && j0 + take < sw.blocks) {
       AttnCut c;
-      c.ends = c.c0 = 0;
-      if (!a.whole && j0 + take < sw.blocks) {
-        const long long u0 = sh.end - units_ - j0;  // the item's first unit
-        c.c0 = static_cast<int>(u0 / sh.per);
-        c.ends = static_cast<int>((u0 + sw.blocks - 1) / sh.per) - c.c0;
-      }
+      const long long u0 = sh.end - units_ - j0;  // the item's first unit
+      c.c0 = static_cast<int>(u0 / sh.per);
+      c.ends = static_cast<int>((u0 + sw.blocks - 1) / sh.per) - c.c0;
       c.q0 = sw.q0;
       c.head = head;
       c.r_first = r_first;
@@ -580,10 +578,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
   griddep_wait();
   griddep_launch_dependents();
   const AttnShare share = attn_share<RT>(a, sched);
-  if (share.begin >= share.end) {
-    if (threadIdx.x == 0) a.cuts[blockIdx.x].ends = 0;
-    return;
-  }
+  if (share.begin >= share.end) return;
 
   uint32_t phase = 0;  // steps this warp has taken before this segment (stage and parity)
   AttnSegment<RT> seg(a, share, wt, lane);
@@ -949,10 +944,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
   griddep_wait();
   griddep_launch_dependents();
   const AttnShare share = attn_share<RT>(a, sched);
-  if (share.begin >= share.end) {
-    if (threadIdx.x == 0) a.cuts[blockIdx.x].ends = 0;
-    return;
-  }
+  if (share.begin >= share.end) return;
 
   uint32_t phase = 0;  // steps this warp has taken before this segment (stage and parity)
   AttnSegment<RT> seg(a, share, wt, lane);
@@ -1203,18 +1195,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
 }
 
 // Joins the partial results of items that several CTAs shared.  Such an item has a CTA's
-// end inside it: kJoinSplit CTAs of this kernel look at the end of each CTA of the first
-// one, and all that look at ends inside one item share its outputs among them.  As many
+// end inside it: four CTAs of this kernel (twelve for tiles of 32 rows of 128 channels) look
+// at the end of each CTA of the first one, and all that look at ends inside one item share its
+// outputs among them.  As many
 // lanes as there are parts (a power of two, at most a warp) take one four of outputs, so
 // that every load is in flight at once; they are added as a tree, the same every time.
-constexpr int kJoinSplit = 4;
+constexpr int join_split(int RT, int D) { return RT * D >= 4096 ? 12 : 4; }
 
 template <int D>
 __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, int RT) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const AttnCut cut = a.cuts[blockIdx.x / kJoinSplit];
+  const int lane = threadIdx.x & 31, split = join_split(RT, D);
+  const AttnCut cut = a.cuts[blockIdx.x / split];
   if (cut.ends == 0) return;
   const int G = a.q_heads / a.kv_heads;
   const int c0 = cut.c0, c1 = c0 + cut.ends;
@@ -1222,8 +1215,8 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
   int lanes = 2;  // to an output
   while (lanes < 32 && lanes <= c1 - c0) lanes *= 2;
   // my piece of the outputs, in fours
-  const int all = cut.rows * (D / 4), pieces = cut.ends * kJoinSplit;
-  const int my = blockIdx.x - c0 * kJoinSplit, end = all * (my + 1) / pieces;
+  const int all = cut.rows * (D / 4), pieces = cut.ends * split;
+  const int my = blockIdx.x - c0 * split, end = all * (my + 1) / pieces;
   for (int base = all * my / pieces; base < end; base += 128 / lanes) {
     const int i = min(base + static_cast<int>(threadIdx.x) / lanes, end - 1);
     const int r = i / (D / 4), d = 4 * (i % (D / 4));
@@ -1316,7 +1309,7 @@ cudaError_t run_attn(Kernel kernel, std::atomic<bool> (&done)[kAttrDevices], int
   const cudaError_t f = launch_pdl(kernel, grid, 32 * kAttnWarps, smem, st, 1, tm_k, tm_v, a);
   if (f != cudaSuccess || a.whole) return f;
   return launch_pdl(D == 128 ? attn_kv8_join_kernel<128> : attn_kv8_join_kernel<64>,
-                    (grid - 1) * kJoinSplit, 128, 0, st, 1, a, RT);
+                    (grid - 1) * join_split(RT, D), 128, 0, st, 1, a, RT);
 }
 
 template <int D>
