@@ -449,6 +449,8 @@ def wq_attn_kv8(q, q_start, kv_len, block_table, k_codes, v_codes, k_scale, v_sc
     dev = _current_device()
     B = kv_len.shape[0]
     cache = _cache_args(k_codes, v_codes, k_scale, v_scale, block_table, B, dev)
+    if len(q.shape) != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [rows, heads, {cache[-1]}]")
     Tq, heads, D = q.shape[0], q.shape[1], cache[-1]
     qp, qs = _row_ptr(q, "q", heads, D, dev)
     _call("wq_attn_kv8", qp, qs, Tq, heads, _ptr(q_start, "q_start", _I32, B + 1, dev),

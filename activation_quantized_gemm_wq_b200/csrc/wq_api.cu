@@ -39,6 +39,7 @@ wq_status check_table(int S, int T, int step) {
 }
 
 constexpr long long kMaxGrid = 2147483647;
+constexpr int kMaxGroupN = 1 << 30;  // rows of group-scaled weights: 32-bit indices
 
 wq_status check_group(int group) {
   return group == 32 || group == 64 || group == 128 ? WQ_OK : WQ_ERR_ARG;
@@ -503,8 +504,7 @@ wq_status wq_pack_int4_group(const wq_bf16* W, const float* c, int N, int K, int
                              uint8_t* qw, wq_bf16* s_g, wq_stream_t stream) {
   WQ_TRY(check_group(group));
   WQ_TRY(check_mk(0, K));
-  if (N < 1 || (static_cast<long long>(N) + 15) / 16 * ((K + 511) / 512) > kMaxGrid)
-    return WQ_ERR_SHAPE;
+  if (N < 1 || N > kMaxGroupN) return WQ_ERR_SHAPE;
   if (!W || !qw || !s_g) return WQ_ERR_NULL;
   if (!aligned16(W) || !aligned16(qw) || !aligned(s_g, 2) || (c && !aligned16(c)))
     return WQ_ERR_ALIGN;
@@ -517,7 +517,7 @@ wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
                       wq_bf16* y, wq_stream_t stream) {
   WQ_TRY(check_group(group));
   WQ_TRY(check_mk(M, K));
-  if (M > wq::kGemvMaxM || N < 1 || N > kMaxGrid - 64) return WQ_ERR_SHAPE;
+  if (M > wq::kGemvMaxM || N < 1 || N > kMaxGroupN) return WQ_ERR_SHAPE;
   if (M == 0) return WQ_OK;
   if (!x || !qw || !s_g || !y) return WQ_ERR_NULL;
   if (!aligned16(x) || !aligned16(qw) || !aligned(s_g, 2) || !aligned(y, 2) ||

@@ -82,6 +82,9 @@ __global__ void __launch_bounds__(128, D == 128 ? 5 : 7) kv8_append_kernel(const
   const uint32_t windows = (a.T + a.window - 1) / a.window;
   griddep_wait();
   griddep_launch_dependents();
+  if (unit == 0)  // the table of rows as a whole, once
+    for (int i = lane; i < a.B; i += 32)
+      if (a.row_start[i] > a.row_start[i + 1]) raise_cache_error();
   if (unit >= windows * a.heads * 2u) return;
   const int which = unit & 1;
   const int head = (unit >> 1) % static_cast<uint32_t>(a.heads);
@@ -100,9 +103,10 @@ __global__ void __launch_bounds__(128, D == 128 ? 5 : 7) kv8_append_kernel(const
       b = find_sequence(a.row_start, a.B, t);
       if (b < 0) return;  // rows outside every sequence are left alone
       first = a.row_start[b];
-      last = min(a.row_start[b + 1], a.T);
+      const int end = a.row_start[b + 1];
+      last = min(end, a.T);
       past = a.past_len[b];
-      if (past < 0 || first < 0 || last <= t ||
+      if (past < 0 || first < 0 || last <= t || end > a.T ||
           static_cast<long long>(past) + (last - first) > capacity) {
         if (lane == 0) raise_cache_error();
         if (last <= t) return;

@@ -357,7 +357,7 @@ wq_status wq_linear_w4a8_noalloc(const wq_bf16* x, int M, int K, int N, const fl
  *   s_g[k/group][n] = bf16(max over the group of |W'[n,k]| / 7)
  *   code[n,k]       = clamp(rint_half_even(W'[n,k] / s_g), -7, 7), 0 where s_g is 0
  * with IEEE fp32 divisions; the codes are decided by the rounded scale.
- *   W [N][K] bf16; group 32, 64 or 128 (else WQ_ERR_ARG); N >= 1;
+ *   W [N][K] bf16; group 32, 64 or 128 (else WQ_ERR_ARG); 1 <= N <= 2^30;
  *   qw [N][K/2] uint8 out; s_g [K/group][N] bf16 out.
  * Layout of qw (not wq_pack_int4's): in each run of 128 channels (64 bytes, sixteen
  * little-endian 32-bit words) word 4t + j, for t, j in 0..3, holds channels
@@ -371,9 +371,10 @@ wq_status wq_pack_int4_group(const wq_bf16* W, const float* c, int N, int K, int
  *   x'[m,k] = fp32(x[m,k]) * cinv[k] (cinv may be NULL, meaning 1)
  * with fp32 sums over the groups.  Up to 8 tokens x' is held in 22 bits below the
  * largest |x'| of its group (off by at most 2^-22 of that, or 2^-128) and a group's sum is
- * exact; beyond 8 tokens x' is rounded to 11 bits (bf16 values themselves are exact) and
- * a group's sum is fp32.
- *   x [M][K] bf16, 0 <= M <= 16; bias [N] fp32 or NULL; y [M][N] bf16 out; any N >= 1.
+ * exact; beyond 8 tokens x' is rounded to 11 bits (bf16 values themselves are exact; values
+ * below 2^-28 of their group's largest to 2^-39 of that) and a group's sum is fp32.
+ *   x [M][K] bf16, 0 <= M <= 16; bias [N] fp32 or NULL; y [M][N] bf16 out;
+ *   1 <= N <= 2^30.
  * No workspace. */
 wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
                       const uint8_t* qw, const wq_bf16* s_g, int group, const float* bias,
@@ -407,7 +408,8 @@ wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
  * contents.
  * Checked on the device: 0 <= past_len, the tokens fit max_pages, the pages used are in
  * [0, pages), row_start does not decrease and stays within [0, T].  A violation sets
- * WQ_DEVICE_ERR_CACHE and writes nothing for that sequence (or page). */
+ * WQ_DEVICE_ERR_CACHE; nothing is written for a sequence that does not fit or whose rows
+ * lie outside [0, T], nor to a page outside the cache. */
 wq_status wq_kv8_append(const wq_bf16* k, const wq_bf16* v, int64_t k_stride, int64_t v_stride,
                         int T, const int32_t* row_start, const int32_t* past_len, int B,
                         const int32_t* block_table, int max_pages, int8_t* k_codes,

@@ -112,7 +112,10 @@ def check_gemv(x, cinv, qw, s_g, group, bias, y):
 @pytest.mark.parametrize("fold", [False, True])
 @pytest.mark.parametrize("M,K,N", [
     (1, 128, 1), (1, 2048, 2048), (2, 384, 15), (3, 1152, 33), (7, 4096, 65), (8, 1024, 257),
-    (9, 256, 16), (13, 8192, 47), (16, 2048, 31), (4, 16384, 129), (1, 32768, 3)])
+    (9, 256, 16), (13, 8192, 47), (16, 2048, 31), (4, 16384, 129), (1, 32768, 3),
+    # several tiles to a CTA; K split over clusters; more staged tokens than a CTA holds
+    (2, 256, 40000), (6, 16384, 700), (5, 32768, 40), (16, 32768, 50), (12, 28672, 20),
+    (11, 1152, 5000)])
 def test_gemv(M, K, N, group, fold):
     g = torch.Generator(device="cuda").manual_seed(M * 7919 + K + N)
     W = (torch.randn(N, K, generator=g, device="cuda") * 0.02).bfloat16()

@@ -151,6 +151,17 @@ def test_append_leaves_other_rows_and_sequences_alone():
     assert wq.wq_device_status() == ("WQ_OK", 0)
 
 
+@pytest.mark.parametrize("starts_bad", [[0, 5, 3, 8], [0, 4, 9], [-2, 4, 8]])
+def test_append_reports_bad_row_tables(starts_bad):
+    """Rows that go back, end behind T or begin before 0: reported, nothing out of bounds."""
+    D, heads, page, B = 64, 1, 16, len(starts_bad) - 1
+    table, pages = page_table([32] * B, page)
+    cache = random_cache(pages, heads, page, D, 6)
+    x = torch.randn(8, heads, D, device="cuda").bfloat16()
+    wq.wq_kv8_append(x, x, ints(starts_bad), ints([0] * B), table, **cache)
+    assert wq.wq_device_status() == ("WQ_ERR_DEVICE", 4)
+
+
 # ---------------------------------------------------------------- attention
 
 def whole(codes, scale, table_row, n):
@@ -255,6 +266,19 @@ def test_attention_of_many_short_sequences():
 def test_attention_with_small_and_large_queries(q_size):
     """Flat softmax, one-hot softmax; queries outside f16's range."""
     run_attention([1, 4], [333, 90], 4, 2, 64, 32, True, seed=2, q_size=q_size)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 3.0])
+@pytest.mark.parametrize("m,Hq,Hkv", [(1, 4, 2), (1, 8, 1), (3, 4, 1), (30, 2, 2)])
+def test_attention_scales(scale, m, Hq, Hkv):
+    """Negative, zero and large softmax scales, in every tile height."""
+    n, D, page = 700, 64, 32
+    table, pages = page_table([n], page, seed=2)
+    cache = random_cache(pages, Hkv, page, D, 8)
+    q = torch.randn(m, Hq, D, generator=torch.Generator(device="cuda").manual_seed(4),
+                    device="cuda").bfloat16()
+    out, lse = attend(q, ints([0, m]), ints([n]), table, cache, True, scale)
+    check_attention(q, [m], [n], table, cache, True, scale, out, lse)
 
 
 def test_attention_rising_scores_and_uneven_value_scales():
