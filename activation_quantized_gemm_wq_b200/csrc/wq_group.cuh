@@ -240,7 +240,8 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
 
 constexpr int kGemvWarps = 16;
 constexpr int kGemvMaxSplit = 8;            // CTAs that share K (a portable cluster)
-constexpr int kGemvMaxSmem = 226 * 1024;
+constexpr int kGemvMaxTiles = 512;          // row tiles of a cluster
+constexpr int kGemvMaxSmem = 224 * 1024;    // dynamic, beside 2 KB of tables
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
@@ -270,7 +271,7 @@ struct GemvArgs {
   int tiles;             // row tiles of a cluster (the last may have fewer)
 };
 
-// MT: 16-channel halves of a row tile; NT: groups of four tokens (1 or 2, digits; 4, f16);
+// MT: 16-channel halves of a row tile; NT: groups of four tokens (1, digits; 2 or 4, f16);
 // TINY: one or two tokens, whose lowest digits fill the columns that hi and mid leave free.
 template <int MT, int NT, bool TINY>
 struct GemvCfg {
@@ -279,8 +280,8 @@ struct GemvCfg {
   static constexpr int STAGES = NT == 4 ? 2 : 3;
   static constexpr int TILE = RPS * WR * 64;
   static constexpr int RING = kGemvWarps * STAGES * TILE;
-  static constexpr bool HALF = NT == 4;            // tokens as f16 instead of digits
-  static constexpr int COLS = HALF ? 4 : TINY ? 1 : NT + 1;  // KB of staged tokens a run
+  static constexpr bool HALF = NT > 1;             // tokens as f16 instead of digits
+  static constexpr int COLS = HALF ? NT : TINY ? 1 : 2;  // KB of staged tokens a run
   static constexpr int TOKENS = TINY ? 2 : 4 * NT;
   static constexpr int SEG = TOKENS * WR;             // floats of a segment's sums
   static constexpr int run_bytes(int group) { return COLS * 1024 + 128 / group * TOKENS * 4; }
@@ -304,19 +305,18 @@ struct GemvCfg {
 // the largest |x'| of their group (a power-of-two scale: a value is off by at most 2^-22 of
 // that maximum, and bf16 values down to 2^-14 of it are exact), split into three signed
 // bytes, hi 2^16 + mid 2^8 + lo.  hi and mid of a token are neighbouring columns of one
-// column tile, so that a lane holds both sums; the lo of eight tokens fill another (TINY:
-// columns 4 and 6).  The sums of a group are exact in int32; they are joined, scaled and
+// column tile, so that a lane holds both sums; the lo fill another (TINY: columns 4 and 6).  The sums of a group are exact in int32; they are joined, scaled and
 // added over the groups in fp32.
 //
 // Staged layout: column tile c, run r: 1 KB [half][column][t][16 bytes], the 16 bytes of
 // half h being the channels of words j = 2h, 2h + 1, in the order 0 4 1 5, 2 6 3 7 in
 // which the masks leave the codes.
 //
-// More than eight tokens (HALF) would need six column tiles and the joining of as many
-// sums, which takes longer than the copies; they enter as f16 instead, 11 bits of x' over
-// a power-of-two scale per group, against codes made f16 (exact; nine instructions for
-// eight codes), two column tiles of eight tokens.  Staged run: 2 KB per column tile,
-// [word j][column][t][8 channels].
+// More than four tokens (HALF) would need three to six column tiles and the joining of as
+// many sums, which takes longer than the copies, as does splitting the tokens; they enter as
+// f16 instead, 11 bits of x' over a power-of-two scale per group, against codes made f16
+// (exact; nine instructions for eight codes), in column tiles of eight tokens.  Staged run:
+// 2 KB per column tile, [word j][column][t][8 channels].
 template <int G, int MT, int NT, bool TINY>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
     const __grid_constant__ CUtensorMap tm_w, const GemvArgs a) {
@@ -324,9 +324,11 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
   constexpr int WR = Cfg::WR, RPS = Cfg::RPS, STAGES = Cfg::STAGES, SEG = Cfg::SEG;
   constexpr int COLS = Cfg::COLS, TOKENS = Cfg::TOKENS;
   constexpr bool HALF = Cfg::HALF;
+  constexpr int CT = NT / 2 > 0 ? NT / 2 : 1;  // HALF: column tiles
   constexpr int THREADS = 32 * kGemvWarps;
   extern __shared__ uint8_t gemv_smem[];
   __shared__ __align__(8) uint64_t full[kGemvWarps][STAGES];
+  __shared__ short2 span[kGemvMaxTiles];  // first and last warp with a segment of a row tile
   uint8_t* ring_all = gemv_smem + ((128u - (smem_u32(gemv_smem) & 127u)) & 127u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int S = a.S, M = a.M, N = a.N;
@@ -346,9 +348,14 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
   float* segs = xscale + a.share * (128 / G) * TOKENS;
 
   if (lane == 0) {
+    if (warp == 0) tma_prefetch_desc(&tm_w);
     for (int s = 0; s < STAGES; ++s) mbar_init(&full[warp][s], 1);
     fence_mbar_init();
   }
+  // Row tile q's segments are those of the warps whose pieces overlap [q, q + 1) per_tile
+  for (int q = threadIdx.x; q < tiles && total > 0; q += THREADS)
+    span[q] = make_short2(static_cast<short>((kGemvWarps * q * per_tile + kGemvWarps - 1) / total),
+                          static_cast<short>((kGemvWarps * (q + 1) * per_tile - 1) / total));
   __syncwarp();
   griddep_wait();
   griddep_launch_dependents();
@@ -370,6 +377,32 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
     }
   };
   for (int i = 0; i < STAGES && i < count; ++i) issue(i);
+
+  // The tokens of this share: a thread takes eight channels, XB times at a time (the loads
+  // of a batch are in flight together, the first batch's while the scales are looked up).
+  // Columns of tokens past M keep what shared memory held: nothing of them is written.
+  constexpr int XB = 4;
+  const int pieces = runs * 16, pieces_all = M * pieces;
+  const uint32_t inv = pieces > 1 ? 0xFFFFFFFFu / pieces + 1 : 0;  // at / pieces, at < 2^18
+  uint4 raw[XB];
+  float4 ci[XB][2];
+  auto fetch_x = [&](int base) {
+#pragma unroll
+    for (int e = 0; e < XB; ++e) {
+      const int at = base + e * THREADS, m = __umulhi(at, inv), pc = at - m * pieces;
+      raw[e] = make_uint4(0, 0, 0, 0);
+      ci[e][0] = ci[e][1] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+      if (at >= pieces_all) continue;
+      raw[e] = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(m) * a.K) +
+                     r_begin * 16 + pc);
+      if (a.cinv) {
+        const float4* cp = reinterpret_cast<const float4*>(a.cinv) + 2 * (r_begin * 16 + pc);
+        ci[e][0] = __ldg(cp);
+        ci[e][1] = __ldg(cp + 1);
+      }
+    }
+  };
+  fetch_x(threadIdx.x);
 
   // scales two stages ahead in registers; lane t: the group of word t
   uint16_t sc[2][RPS][MT][2];
@@ -407,32 +440,19 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
     if (count > 1) load_scales(sc[1]);
   }
 
-  // The tokens of this share: a thread takes eight channels, XB times at a time (the loads
-  // of a batch are in flight together); the G / 8 threads of a group are neighbours and
-  // share its maximum by shuffles.  Tokens past M become zeros.
+  // the G / 8 threads of a group are neighbours and share its maximum by shuffles
   {
-    constexpr int XB = 4;
-    const int pieces = runs * 16, pieces_all = TOKENS * pieces;
-    const uint32_t inv = pieces > 1 ? 0xFFFFFFFFu / pieces + 1 : 0;  // at / pieces, at < 2^18
-    for (int base = threadIdx.x; base - static_cast<int>(threadIdx.x) < pieces_all;
-         base += XB * THREADS) {
-      uint4 raw[XB];
+    for (int base0 = 0; base0 < pieces_all; base0 += XB * THREADS) {
+      const int base = base0 + threadIdx.x;
 #pragma unroll
       for (int e = 0; e < XB; ++e) {
-        const int at = base + e * THREADS, m = __umulhi(at, inv), pc = at - m * pieces;
-        raw[e] = make_uint4(0, 0, 0, 0);
-        if (at < pieces_all && m < M)
-          raw[e] = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(m) * a.K) +
-                         r_begin * 16 + pc);
-      }
-#pragma unroll
-      for (int e = 0; e < XB; ++e) {
-        if (base - static_cast<int>(threadIdx.x) + e * THREADS >= pieces_all) break;  // uniform
+        if (base0 + e * THREADS >= pieces_all) break;  // uniform
         const int at = base + e * THREADS, m = __umulhi(at, inv), pc = at - m * pieces;
         const bool valid = at < pieces_all;
-        float ci[8], v[8];
-        load_cinv8_global(valid ? a.cinv : nullptr, r_begin * 16 + pc, ci);
-        scale8(raw[e], ci, v);
+        const float cf[8] = {ci[e][0].x, ci[e][0].y, ci[e][0].z, ci[e][0].w,
+                             ci[e][1].x, ci[e][1].y, ci[e][1].z, ci[e][1].w};
+        float v[8];
+        scale8(raw[e], cf, v);
         float top = 0.0f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(v[c]));
@@ -443,7 +463,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
         const uint32_t ex = max(__float_as_uint(top) >> 23, BITS);
         const float up = __uint_as_float((254u + BITS - ex) << 23);
         if (!valid) continue;
-        const int run = pc >> 4, j = (pc >> 2) & 3, tt = pc & 3, nt = m >> 2;
+        const int run = pc >> 4, j = (pc >> 2) & 3, tt = pc & 3;
         uint8_t* dst = xs + run * (COLS * 1024);
         if constexpr (HALF) {
           *reinterpret_cast<uint4*>(dst + (m >> 3) * 2048 + j * 512 + (m & 7) * 64 + tt * 16) =
@@ -458,8 +478,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
           dst += (j >> 1) * 512 + tt * 16 + (j & 1) * 8;
 #pragma unroll
           for (int b = 0; b < 3; ++b) {
-            const int tile = TINY ? 0 : b == 0 ? NT : nt;
-            const int col = 2 * (m & 3) + (b > 0 ? 2 - b : TINY ? 4 : nt & 1);
+            const int tile = !TINY && b == 0 ? 1 : 0;
+            const int col = 2 * (m & 3) + (b > 0 ? 2 - b : TINY ? 4 : 0);
             *reinterpret_cast<uint2*>(dst + tile * 1024 + col * 64) =
                 make_uint2(gather_bytes(d[0], d[4], d[1], d[5], b),
                            gather_bytes(d[2], d[6], d[3], d[7], b));
@@ -470,6 +490,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
           xscale[pc / (G / 8) * TOKENS + m] =
               __uint_as_float((ex - BITS + 1u) << 23) * (HALF ? 0.5f : 0.03125f);
       }
+      if (base0 + XB * THREADS < pieces_all) fetch_x(base + XB * THREADS);
     }
   }
   __syncthreads();
@@ -501,12 +522,12 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
         return __uint_as_float(G == 128 ? v : __shfl_sync(0xFFFFFFFFu, v, (lane & 28) | j));
       };
       if constexpr (HALF) {
-        float sum[MT][2][4] = {};
+        float sum[MT][CT][4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint4 b[2];
+          uint4 b[CT];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < CT; ++c)
             b[c] = *reinterpret_cast<const uint4*>(xp + c * 2048 + j * 512);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -516,15 +537,15 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
                                    codes_f16x2<1>(wb), codes_f16x2<0>(va), codes_f16x2<0>(vb),
                                    codes_f16x2<1>(va), codes_f16x2<1>(vb)};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < CT; ++c) {
               mma_f16(sum[mt][c], f[0], f[1], f[2], f[3], b[c].x, b[c].y);
               mma_f16(sum[mt][c], f[4], f[5], f[6], f[7], b[c].z, b[c].w);
             }
           }
           if ((j + 1) % (G / 32) == 0) {  // the group ends
-            float2 fx[2];
+            float2 fx[CT];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < CT; ++c)
               fx[c] = *reinterpret_cast<const float2*>(xf + j / (G / 32) * TOKENS + 8 * c);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -532,7 +553,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
               for (int h = 0; h < 2; ++h) {
                 const float fw = row_scale(mt, h, j);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {  // (fw * fx may underflow)
+                for (int c = 0; c < CT; ++c) {  // (fw * fx may underflow)
                   float* q = &sum[mt][c][2 * h];
                   acc[mt][2 * c][h] = fmaf(q[0] * fx[c].x, fw, acc[mt][2 * c][h]);
                   acc[mt][2 * c + 1][h] = fmaf(q[1] * fx[c].y, fw, acc[mt][2 * c + 1][h]);
@@ -563,24 +584,19 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
                        j % (G / 32) == 0);
             }
             if ((j + 1) % (G / 32) == 0) {  // the group ends
-              float fx[NT];
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) fx[nt] = xf[j / (G / 32) * TOKENS + 4 * nt];
+              const float fx = xf[j / (G / 32) * TOKENS];
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float fw = row_scale(mt, h, j);
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    const int* hm = sum[mt][nt] + 2 * h;
-                    const int low = TINY ? __shfl_xor_sync(0xFFFFFFFFu, hm[0], 2)
-                                         : sum[mt][COLS - 1][2 * h + (nt & 1)];
-                    const float v24 = fmaf(static_cast<float>(hm[0]), 65536.0f,
-                                           static_cast<float>(hm[1] * 256 + low));
-                    // (fw * fx may underflow)
-                    acc[mt][nt][h] = fmaf(v24 * fx[nt], fw, acc[mt][nt][h]);
-                  }
+                  const int* hm = sum[mt][0] + 2 * h;
+                  const int low = TINY ? __shfl_xor_sync(0xFFFFFFFFu, hm[0], 2)
+                                       : sum[mt][COLS - 1][2 * h];
+                  const float v24 = fmaf(static_cast<float>(hm[0]), 65536.0f,
+                                         static_cast<float>(hm[1] * 256 + low));
+                  // (fw * fx may underflow)
+                  acc[mt][0][h] = fmaf(v24 * fx, fw, acc[mt][0][h]);
                 }
             }
           }
@@ -616,14 +632,13 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
       mbar_wait_drain(&full[warp][q % STAGES], (q / STAGES) & 1);
   __syncthreads();
 
-  // Row tile q's segments are those of the warps whose pieces overlap [q, q + 1) per_tile;
-  // segment (tile, warp) lies at tile + warp.
+  // segment (tile, warp) lies at tile + warp
   auto tile_sum = [&](int q, int at) {
-    const int lo = (kGemvWarps * q * per_tile + kGemvWarps - 1) / total;
-    const int hi = (kGemvWarps * (q + 1) * per_tile - 1) / total;
+    const short2 w01 = span[q];
     float v = 0.0f;
-    for (int w = lo; w <= hi; ++w)
-      if (total * w / kGemvWarps < total * (w + 1) / kGemvWarps) v += segs[(q + w) * SEG + at];
+    for (int w = w01.x; w <= w01.y; ++w)
+      if (total >= kGemvWarps || total * w / kGemvWarps < total * (w + 1) / kGemvWarps)
+        v += segs[(q + w) * SEG + at];
     return v;
   };
   float* part = reinterpret_cast<float*>(ring_all);  // [tile][token][channel]
@@ -670,7 +685,8 @@ constexpr int gemv_tiles_limit(int share) {
   using Cfg = GemvCfg<MT, NT, TINY>;
   const int by_ring = Cfg::RING / (Cfg::SEG * 4);
   const int by_smem = (kGemvMaxSmem - Cfg::smem(share, G, 0)) / (Cfg::SEG * 4);
-  return by_ring < by_smem ? by_ring : by_smem;
+  const int most = by_ring < by_smem ? by_ring : by_smem;
+  return most < kGemvMaxTiles ? most : kGemvMaxTiles;
 }
 
 // Clusters of S CTAs, one CTA per SM, that run at the same time on the current device (a
@@ -725,6 +741,7 @@ cudaError_t run_gemv(const uint16_t* x, const float* cinv, const uint8_t* qw, co
     int take = (tiles + clusters - 1) / clusters;
     if (take > limit) take = limit;
     const long long waves = ((tiles + take - 1) / take + clusters - 1) / clusters;
+    take = static_cast<int>((tiles + clusters * waves - 1) / (clusters * waves));  // even waves
     const long long cost = waves * (4LL * take * share * MT + Cfg::TOKENS * share + (c > 1 ? 184 : 0));
     if (S == 0 || cost < best) {
       best = cost;

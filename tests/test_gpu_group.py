@@ -84,8 +84,8 @@ def check_gemv(x, cinv, qw, s_g, group, bias, y):
     """y against 64-bit sums.  One rounding to bf16 (half a step: 2^-8 relative, and the
     subnormals' 2^-134); fp32 sums over the K / group groups and at most 8 parts, with four
     operations to a group's term, each within 2^-24 of the sum of magnitudes; and, up to
-    eight tokens, x' held to 2^-22 of its group's largest (or 2^-128), summed exactly; beyond
-    eight, x' in f16 (2^-11 relative, exact for bf16 itself; 2^-39 of the group's largest
+    four tokens, x' held to 2^-22 of its group's largest (or 2^-128), summed exactly; beyond
+    four, x' in f16 (2^-11 relative, exact for bf16 itself; 2^-39 of the group's largest
     where that is subnormal) and at most 8 matrix steps to a group's sum, each within 2^-22."""
     x8 = x.double()
     if cinv is not None:
@@ -98,7 +98,7 @@ def check_gemv(x, cinv, qw, s_g, group, bias, y):
         ref, size = ref + bias.double(), size + bias.double().abs()
     K = x.shape[1]
     top = x8.abs().view(-1, K // group, group).amax(-1).repeat_interleave(group, 1)
-    few = x.shape[0] <= 8
+    few = x.shape[0] <= 4
     held = (top * 2.0 ** (-22 if few else -39) + 2.0 ** -128) @ w.abs().t()
     steps = (K / group + 8 + 4) * 2.0 ** -24
     if not few:
