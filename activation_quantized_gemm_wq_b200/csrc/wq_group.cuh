@@ -72,6 +72,10 @@ __device__ __forceinline__ uint32_t group_word(const uint32_t (&c)[8]) {
 // scale is rounded to bf16 (2 bytes beside 16 to 64 bytes of codes) BEFORE the codes are
 // decided, so the codes belong to the scale that is stored; a scale rounded down by at most
 // 2^-9 sends the maximum to 7.02, which is 7.
+// Persistent CTAs that load the next tile while this one is made: the issue of instructions
+// (56 % of cycles) and the memory bound it together.  16384 x 4096, groups of 64, with c:
+// 36.0 us, 4.7 TB/s read and written (48.0 us with a CTA per tile, nothing loaded ahead);
+// 2048 x 2048: 3.6 us.
 template <int G, bool SCALED>
 __global__ void __launch_bounds__(256, 2) pack_int4_group_kernel(
     const uint16_t* __restrict__ W, const float* __restrict__ c, int N, int K, int strips,
@@ -305,8 +309,9 @@ struct GemvCfg {
 // the largest |x'| of their group (a power-of-two scale: a value is off by at most 2^-22 of
 // that maximum, and bf16 values down to 2^-14 of it are exact), split into three signed
 // bytes, hi 2^16 + mid 2^8 + lo.  hi and mid of a token are neighbouring columns of one
-// column tile, so that a lane holds both sums; the lo fill another (TINY: columns 4 and 6).  The sums of a group are exact in int32; they are joined, scaled and
-// added over the groups in fp32.
+// column tile, so that a lane holds both sums; the lo fill another (TINY: columns 4 and 6).
+// The sums of a group are exact in int32; they are joined, scaled and added over the groups
+// in fp32.
 //
 // Staged layout: column tile c, run r: 1 KB [half][column][t][16 bytes], the 16 bytes of
 // half h being the channels of words j = 2h, 2h + 1, in the order 0 4 1 5, 2 6 3 7 in
@@ -317,6 +322,14 @@ struct GemvCfg {
 // f16 instead, 11 bits of x' over a power-of-two scale per group, against codes made f16
 // (exact; nine instructions for eight codes), in column tiles of eight tokens.  Staged run:
 // 2 KB per column tile, [word j][column][t][8 channels].
+//
+// Measured (calls in a graph, nothing in L2): 1 token, 2048 x 2048, groups of 128, 4.1 us;
+// 1 token, 4096 -> 12288, 8.1 us, 3.2 TB/s, of which the stream is 4 to 5 us and the rest the
+// start (the tokens, the scales, the first stage) and the joining; 8 tokens, 16384 -> 4096,
+// groups of 64, cinv, 18.9 us, 1.9 TB/s; 16 tokens, 8192 -> 8191, groups of 32, 22.7 us,
+// 1.7 TB/s: there the staging of the tokens in every CTA, the conversions and the exchange
+// count, not the copies.  Weights loaded straight into registers, without the rings, took
+// 12.3 us for the second, 40 and 28 us for the last two.
 template <int G, int MT, int NT, bool TINY>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
     const __grid_constant__ CUtensorMap tm_w, const GemvArgs a) {

@@ -72,7 +72,11 @@ struct AppendArgs {
 // tokens came.  IEEE fp32 throughout: codes and scales are reproducible bit for bit.
 // A block is handled by the warp whose window holds its first new token; the window is
 // one row for decoding (a warp per new token) and 16 rows for long runs (about one block
-// per warp, and no warps that find nothing).
+// per warp, and no warps that find nothing).  The issue of instructions (54 % of cycles; about
+// 650 for a block) and the latency of a block's loads bound it: 3 sequences of up to 4256
+// tokens, 32 heads of 128, 54.9 us, 4.2 TB/s read and written; 32 single tokens, 8 heads,
+// 3.3 us.  Exact quotients by two remainder steps, without a test for near ties, and 32-bit
+// indices within a page took the first from 109 to 60 us, five CTAs to an SM below 55.
 template <int D>
 __global__ void __launch_bounds__(128, D == 128 ? 5 : 7) kv8_append_kernel(const AppendArgs a) {
   constexpr int TC = D / 8;                        // 8-channel chunks of a token
@@ -225,7 +229,8 @@ constexpr int kAttnMinUnits = 16;  // blocks of 16 tokens a CTA takes at least
 // Softmax weights enter the second product in f16 as 2^kPShift times their value
 // relative to a reference maximum that the running one may exceed by up to 2^kPSlack
 // before the sums are rescaled: at most 2^15 (f16 reaches 65504), full 11 bits down to
-// 2^-25 of the reference.
+// 2^-25 of the reference, and steps of 2^-35 of it below.  (8 bits of bf16 would do without
+// the shift, at eight times the rounding error; f32 weights cannot enter the instruction.)
 constexpr float kPShift = 11.0f, kPSlack = 4.0f;
 
 struct AttnArgs {
@@ -535,6 +540,11 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
 // per row that keeps all its 8 bits; scores, maxima, sums and the output are fp32.  Block
 // scales multiply the scores (keys) and the softmax weights relative to a power-of-two
 // reference (values).
+// Eight warps to an SM (247 registers) issue in a third of all cycles: the chain of copies'
+// arrival, conversion, matrix steps and softmax bounds it, not the tensor cores (22 %) nor
+// memory (11 %).  2 x 64 queries over up to 8512 tokens, 32 heads of 64: 55.2 us (58.1 with
+// MT = 1, 83.5 with the first, simple kernel).  Making the codes f16 once per CTA in shared
+// memory for 64 rows was 3 % faster there, but 4 to 7 % slower for heads of 128.
 template <int D, int MT>
 struct AttnCfg {
   static constexpr int WT = kAttnWarps;
@@ -907,6 +917,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
 // A step is two blocks (32 tokens): the maxima, the reference and the barrier are looked
 // at once for both.  The first step of the next segment is fetched while this one's sums
 // are joined (in the other stage of each warp's ring).
+// Long contexts are bound by memory, after about 10 us of start, segments' ends and joining:
+// one token each, four query heads to a cache head of 128: 32 sequences of up to 8192 tokens
+// 60.7 us, 5.2 TB/s; 2 of up to 131072 71.0 us, 5.3 TB/s; 8 of 131072 reach 6.2 TB/s.  A single
+// sequence of up to 500 tokens, 16 heads, takes 9.0 us, all of it latency.  (The first, simple
+// kernel: 84.0, 87.6 and 11.1 us.)
 template <int D, int RT_>
 struct AttnFewCfg {
   static constexpr int RT = RT_, WT = kAttnWarps, TILE = kBlockTokens * D;
@@ -1201,9 +1216,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
 // Joins the partial results of items that several CTAs shared.  Such an item has a CTA's
 // end inside it: four CTAs of this kernel (twelve for tiles of 32 rows of 128 channels) look
 // at the end of each CTA of the first one, and all that look at ends inside one item share its
-// outputs among them.  As many
-// lanes as there are parts (a power of two, at most a warp) take one four of outputs, so
-// that every load is in flight at once; they are added as a tree, the same every time.
+// outputs among them.  As many lanes as there are parts (a power of two, at most a warp) take
+// one four of outputs, so that every load is in flight at once; they are added as a tree, the
+// same every time.  Latency bounds it: with one thread to an output, its parts one after the
+// other, 2 x 131072 tokens took 83.9 us in all instead of 73.  Sixteen CTAs to an end of tiles
+// of 32 rows of 64 channels: 57.3 us for the chunk of 64 queries instead of 55.1 with four.
 constexpr int join_split(int RT, int D) { return RT * D >= 4096 ? 12 : 4; }
 
 template <int D>

@@ -175,7 +175,7 @@ def whole(codes, scale, table_row, n):
 def check_attention(q, q_lens, kv_lens, table, cache, causal, scale, out, lse, first=0):
     """out and lse against 64-bit sums.  One rounding of out to bf16 (2^-8 of it); for the
     sums of p v, in units of sum p|v| / sum p: the weights' rounding to f16 (2^-11, and
-    those below 2^-25 of the largest are held to 2^-40 of it), scores in fp32 (products
+    those below 2^-25 of the largest, steps of 2^-35 of it, by at most 2^-36), scores in fp32 (products
     exact, D / 16 matrix steps, two scalings and the exponential's 2^-22, each relative to
     the sum of magnitudes), and fp32 additions over the blocks."""
     Hq, D = q.shape[1:]
