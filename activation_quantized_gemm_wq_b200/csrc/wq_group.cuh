@@ -263,6 +263,13 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* desc, ui
       : "memory");
 }
 
+// The larger one, or NaN if one is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 struct GemvArgs {
   const uint16_t* x;     // bf16 [M][K]
   const float* cinv;     // [K] or null
@@ -468,9 +475,10 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
         scale8(raw[e], cf, v);
         float top = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(v[c]));
+        for (int c = 0; c < 8; ++c) top = max_or_nan(top, fabsf(v[c]));
 #pragma unroll
-        for (int o = G / 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        for (int o = G / 16; o > 0; o >>= 1)
+          top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
         // digits: 2^(21 - E) with 2^E <= top < 2^(E + 1); f16: 2^(14 - E); at most 2^127
         constexpr uint32_t BITS = HALF ? 14 : 21;
         const uint32_t ex = max(__float_as_uint(top) >> 23, BITS);
@@ -498,10 +506,12 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
                            gather_bytes(d[2], d[6], d[3], d[7], b));
           }
         }
-        // 2^(E - BITS), and the digits' 1 / 16 of the codes
+        // 2^(E - BITS), and the digits' 1 / 16 of the codes; digits cannot hold an x' that
+        // left fp32's range, so their scale says it (f16 holds infinities itself)
         if (pc % (G / 8) == 0)
           xscale[pc / (G / 8) * TOKENS + m] =
-              __uint_as_float((ex - BITS + 1u) << 23) * (HALF ? 0.5f : 0.03125f);
+              !HALF && ex == 255u ? __uint_as_float(0x7FC00000u)
+                                  : __uint_as_float((ex - BITS + 1u) << 23) * (HALF ? 0.5f : 0.03125f);
       }
       if (base0 + XB * THREADS < pieces_all) fetch_x(base + XB * THREADS);
     }

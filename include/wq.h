@@ -373,6 +373,8 @@ wq_status wq_pack_int4_group(const wq_bf16* W, const float* c, int N, int K, int
  * largest |x'| of its group (off by at most 2^-22 of that, or 2^-128) and a group's sum is
  * exact; beyond 4 tokens x' is rounded to 11 bits (bf16 values themselves are exact; values
  * below 2^-28 of their group's largest to 2^-39 of that) and a group's sum is fp32.
+ * A token with an x' beyond fp32's range gets infinities or NaN, the others are not
+ * touched by it.
  *   x [M][K] bf16, 0 <= M <= 16; bias [N] fp32 or NULL; y [M][N] bf16 out;
  *   1 <= N <= 2^30.
  * No workspace. */

@@ -156,6 +156,25 @@ def test_gemv_of_extreme_values():
     check_gemv(x, None, qw, s_g, group, None, gemv(x, None, qw, s_g, group, None))
 
 
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 16])
+def test_gemv_of_products_beyond_the_range_is_not_finite(M, group):
+    """x and cinv are finite, x * cinv is not: every y of that token says so, and the other
+    tokens have what they have without it."""
+    K, N = 512, 48
+    g = torch.Generator().manual_seed(M)
+    qw, s_g = packed(torch.randn(N, K, generator=g).bfloat16(), None, group)
+    x = torch.randn(M, K, generator=g).bfloat16().cuda()
+    cinv = torch.ones(K, device="cuda")
+    cinv[77] = 16.0
+    calm = gemv(x, cinv, qw, s_g, group, None)
+    x[M // 2, 77] = 3e38
+    y = gemv(x, cinv, qw, s_g, group, None)
+    assert not bool(torch.isfinite(y[M // 2]).any())
+    others = [m for m in range(M) if m != M // 2]
+    assert torch.equal(y[others], calm[others])
+
+
 def test_gemv_leaves_what_it_does_not_own():
     """Nothing is written behind y, whatever its alignment, and nothing is read behind qw."""
     K, N, group = 256, 21, 64
