@@ -283,16 +283,18 @@ struct GemvArgs {
 };
 
 // MT: 16-channel halves of a row tile; NT: groups of four tokens (1, digits; 2 or 4, f16);
-// TINY: one or two tokens, whose lowest digits fill the columns that hi and mid leave free.
-template <int MT, int NT, bool TINY>
+// TINY: one or two tokens, whose lowest digits fill the columns that hi and mid leave free;
+// TWO: tokens as two f16 parts, for x * cinv (NT > 1).
+template <int MT, int NT, bool TINY, bool TWO>
 struct GemvCfg {
   static constexpr int WR = 16 * MT;               // output channels of a row tile
   static constexpr int RPS = MT == 1 ? 2 : 1;      // runs per stage (2 KB tiles)
-  static constexpr int STAGES = NT == 4 ? 2 : 3;
+  static constexpr int STAGES = NT == 4 || TWO ? 2 : 3;
   static constexpr int TILE = RPS * WR * 64;
   static constexpr int RING = kGemvWarps * STAGES * TILE;
   static constexpr bool HALF = NT > 1;             // tokens as f16 instead of digits
-  static constexpr int COLS = HALF ? NT : TINY ? 1 : 2;  // KB of staged tokens a run
+  static constexpr int PARTS = TWO ? 2 : 1;
+  static constexpr int COLS = HALF ? NT * PARTS : TINY ? 1 : 2;  // KB of staged tokens a run
   static constexpr int TOKENS = TINY ? 2 : 4 * NT;
   static constexpr int SEG = TOKENS * WR;             // floats of a segment's sums
   static constexpr int run_bytes(int group) { return COLS * 1024 + 128 / group * TOKENS * 4; }
@@ -326,21 +328,25 @@ struct GemvCfg {
 //
 // More than four tokens (HALF) would need three to six column tiles and the joining of as
 // many sums, which takes longer than the copies, as does splitting the tokens; they enter as
-// f16 instead, 11 bits of x' over a power-of-two scale per group, against codes made f16
-// (exact; nine instructions for eight codes), in column tiles of eight tokens.  Staged run:
-// 2 KB per column tile, [word j][column][t][8 channels].
+// f16 instead, over a power-of-two scale per group, against codes made f16 (exact; nine
+// instructions for eight codes), in column tiles of eight tokens.  The 11 bits of f16 hold
+// bf16 tokens exactly.  x * cinv has 24 bits: it enters as two f16 parts (TWO), the second
+// what the first leaves over, which are multiplied by the same codes into the same sums;
+// it is then off by at most 2^-22 of itself, or 2^-39 of its group's largest.  Staged run:
+// [part] 2 KB per column tile, [word j][column][t][8 channels].
 //
 // Measured (calls in a graph, nothing in L2): 1 token, 2048 x 2048, groups of 128, 4.1 us;
 // 1 token, 4096 -> 12288, 8.1 us, 3.2 TB/s, of which the stream is 4 to 5 us and the rest the
 // start (the tokens, the scales, the first stage) and the joining; 8 tokens, 16384 -> 4096,
-// groups of 64, cinv, 18.9 us, 1.9 TB/s; 16 tokens, 8192 -> 8191, groups of 32, 22.7 us,
-// 1.7 TB/s: there the staging of the tokens in every CTA, the conversions and the exchange
-// count, not the copies.  Weights loaded straight into registers, without the rings, took
-// 12.3 us for the second, 40 and 28 us for the last two.
-template <int G, int MT, int NT, bool TINY>
+// groups of 64, cinv, 19.5 us, 1.8 TB/s (18.9 us with 11 bits of x * cinv); 16 tokens,
+// 8192 -> 8191, groups of 32, 22.5 us, 1.7 TB/s: there the staging of the tokens in every CTA,
+// the conversions and the exchange count, not the copies.  Weights loaded straight into
+// registers, without the rings, took 2.8 us for the first, whose warps have one stage or two,
+// but 12.3 us for the second and 40 and 28 us for the last two.
+template <int G, int MT, int NT, bool TINY, bool TWO>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
     const __grid_constant__ CUtensorMap tm_w, const GemvArgs a) {
-  using Cfg = GemvCfg<MT, NT, TINY>;
+  using Cfg = GemvCfg<MT, NT, TINY, TWO>;
   constexpr int WR = Cfg::WR, RPS = Cfg::RPS, STAGES = Cfg::STAGES, SEG = Cfg::SEG;
   constexpr int COLS = Cfg::COLS, TOKENS = Cfg::TOKENS;
   constexpr bool HALF = Cfg::HALF;
@@ -487,9 +493,21 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
         const int run = pc >> 4, j = (pc >> 2) & 3, tt = pc & 3;
         uint8_t* dst = xs + run * (COLS * 1024);
         if constexpr (HALF) {
-          *reinterpret_cast<uint4*>(dst + (m >> 3) * 2048 + j * 512 + (m & 7) * 64 + tt * 16) =
-              make_uint4(pack_half2(v[0] * up, v[1] * up), pack_half2(v[2] * up, v[3] * up),
-                         pack_half2(v[4] * up, v[5] * up), pack_half2(v[6] * up, v[7] * up));
+          dst += (m >> 3) * 2048 + j * 512 + (m & 7) * 64 + tt * 16;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] *= up;
+          const uint32_t h[4] = {pack_half2(v[0], v[1]), pack_half2(v[2], v[3]),
+                                 pack_half2(v[4], v[5]), pack_half2(v[6], v[7])};
+          *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+          if constexpr (TWO) {  // what is left over: exact, then rounded to 11 bits of its own
+            uint32_t rest[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[c]));
+              rest[c] = pack_half2(v[2 * c] - f.x, v[2 * c + 1] - f.y);
+            }
+            *reinterpret_cast<uint4*>(dst + CT * 2048) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+          }
         } else {
           uint32_t d[8];
 #pragma unroll
@@ -548,9 +566,9 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
         float sum[MT][CT][4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint4 b[CT];
+          uint4 b[Cfg::PARTS * CT];
 #pragma unroll
-          for (int c = 0; c < CT; ++c)
+          for (int c = 0; c < Cfg::PARTS * CT; ++c)
             b[c] = *reinterpret_cast<const uint4*>(xp + c * 2048 + j * 512);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -560,9 +578,9 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
                                    codes_f16x2<1>(wb), codes_f16x2<0>(va), codes_f16x2<0>(vb),
                                    codes_f16x2<1>(va), codes_f16x2<1>(vb)};
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              mma_f16(sum[mt][c], f[0], f[1], f[2], f[3], b[c].x, b[c].y);
-              mma_f16(sum[mt][c], f[4], f[5], f[6], f[7], b[c].z, b[c].w);
+            for (int c = 0; c < Cfg::PARTS * CT; ++c) {
+              mma_f16(sum[mt][c % CT], f[0], f[1], f[2], f[3], b[c].x, b[c].y);
+              mma_f16(sum[mt][c % CT], f[4], f[5], f[6], f[7], b[c].z, b[c].w);
             }
           }
           if ((j + 1) % (G / 32) == 0) {  // the group ends
@@ -703,9 +721,9 @@ bool group_map(CUtensorMap* m, const void* base, int K, int N, int rows, int run
 
 // Row tiles a cluster may take at most: their joined sums lie over the ring, and their
 // segments beside the staged tokens.
-template <int G, int MT, int NT, bool TINY>
+template <int G, int MT, int NT, bool TINY, bool TWO>
 constexpr int gemv_tiles_limit(int share) {
-  using Cfg = GemvCfg<MT, NT, TINY>;
+  using Cfg = GemvCfg<MT, NT, TINY, TWO>;
   const int by_ring = Cfg::RING / (Cfg::SEG * 4);
   const int by_smem = (kGemvMaxSmem - Cfg::smem(share, G, 0)) / (Cfg::SEG * 4);
   const int most = by_ring < by_smem ? by_ring : by_smem;
@@ -743,13 +761,13 @@ int gemv_clusters(Kernel kernel, int S) {
   return n;
 }
 
-template <int G, int MT, int NT, bool TINY>
+template <int G, int MT, int NT, bool TINY, bool TWO>
 cudaError_t run_gemv(const uint16_t* x, const float* cinv, const uint8_t* qw, const uint16_t* s_g,
                      const float* bias, uint16_t* y, int M, int K, int N, cudaStream_t st) {
-  using Cfg = GemvCfg<MT, NT, TINY>;
+  using Cfg = GemvCfg<MT, NT, TINY, TWO>;
   const int runs = K / 128, tiles = (N + Cfg::WR - 1) / Cfg::WR;
   static std::atomic<bool> done[kAttrDevices];
-  const cudaError_t e = set_smem_once(gemv_w4g_kernel<G, MT, NT, TINY>, kGemvMaxSmem, done);
+  const cudaError_t e = set_smem_once(gemv_w4g_kernel<G, MT, NT, TINY, TWO>, kGemvMaxSmem, done);
   if (e != cudaSuccess) return e;
   // The split of K, by what an SM has to do, in KB of weights: the tiles of its clusters,
   // staging its share of the tokens (each takes about as long as a quarter of a KB per
@@ -758,9 +776,9 @@ cudaError_t run_gemv(const uint16_t* x, const float* cinv, const uint8_t* qw, co
   long long best = 0;
   for (int c = 1; c <= kGemvMaxSplit && c <= runs; c *= 2) {
     const int share = (runs + c - 1) / c;
-    const int limit = gemv_tiles_limit<G, MT, NT, TINY>(share);
+    const int limit = gemv_tiles_limit<G, MT, NT, TINY, TWO>(share);
     if (limit < 1) continue;
-    const int clusters = gemv_clusters(gemv_w4g_kernel<G, MT, NT, TINY>, c);
+    const int clusters = gemv_clusters(gemv_w4g_kernel<G, MT, NT, TINY, TWO>, c);
     int take = (tiles + clusters - 1) / clusters;
     if (take > limit) take = limit;
     const long long waves = ((tiles + take - 1) / take + clusters - 1) / clusters;
@@ -778,7 +796,7 @@ cudaError_t run_gemv(const uint16_t* x, const float* cinv, const uint8_t* qw, co
   if (!group_map(&tm, qw, K, N, Cfg::WR, Cfg::RPS)) return cudaErrorInvalidValue;
   const GemvArgs a{x, cinv, s_g, bias, y, M, K, N, S, share, per_cluster};
   const int grid = (tiles + per_cluster - 1) / per_cluster * S;
-  return launch_pdl(gemv_w4g_kernel<G, MT, NT, TINY>, grid, 32 * kGemvWarps,
+  return launch_pdl(gemv_w4g_kernel<G, MT, NT, TINY, TWO>, grid, 32 * kGemvWarps,
                     Cfg::smem(share, G, per_cluster), st, S, tm, a);
 }
 
@@ -789,16 +807,20 @@ cudaError_t dispatch_gemv(const uint16_t* x, const float* cinv, const uint8_t* q
   // the largest split must hold the staged tokens; where it cannot (more than 8 tokens of
   // long rows), 8 tokens at a time
   const int share = (K / 128 + kGemvMaxSplit - 1) / kGemvMaxSplit;
-  const int most = M > 8 && gemv_tiles_limit<G, 2, 4, false>(share) < 4 ? 8 : M;
+  const int limit = cinv ? gemv_tiles_limit<G, 2, 4, false, true>(share)
+                         : gemv_tiles_limit<G, 2, 4, false, false>(share);
+  const int most = M > 8 && limit < 4 ? 8 : M;
   for (int m = 0; m < M; m += most) {
     const int n = M - m < most ? M - m : most;
     const uint16_t* xm = x + static_cast<size_t>(m) * K;
     uint16_t* ym = y + static_cast<size_t>(m) * N;
     const cudaError_t e =
-        n <= 2   ? run_gemv<G, 1, 1, true>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
-        : n <= 4 ? run_gemv<G, 2, 1, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
-        : n <= 8 ? run_gemv<G, 2, 2, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
-                 : run_gemv<G, 2, 4, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st);
+        n <= 2   ? run_gemv<G, 1, 1, true, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
+        : n <= 4 ? run_gemv<G, 2, 1, false, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
+        : n <= 8 ? (cinv ? run_gemv<G, 2, 2, false, true>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
+                         : run_gemv<G, 2, 2, false, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st))
+        : cinv   ? run_gemv<G, 2, 4, false, true>(xm, cinv, qw, s_g, bias, ym, n, K, N, st)
+                 : run_gemv<G, 2, 4, false, false>(xm, cinv, qw, s_g, bias, ym, n, K, N, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -369,10 +369,10 @@ wq_status wq_pack_int4_group(const wq_bf16* W, const float* c, int N, int K, int
 /* The weight-only linear for one to a few tokens, on wq_pack_int4_group's weights:
  *   y[m,n] = bf16( sum_k x'[m,k] * s_g[k/group][n] * code[n,k] + bias[n] )
  *   x'[m,k] = fp32(x[m,k]) * cinv[k] (cinv may be NULL, meaning 1)
- * with fp32 sums over the groups.  Up to 4 tokens x' is held in 22 bits below the
- * largest |x'| of its group (off by at most 2^-22 of that, or 2^-128) and a group's sum is
- * exact; beyond 4 tokens x' is rounded to 11 bits (bf16 values themselves are exact; values
- * below 2^-28 of their group's largest to 2^-39 of that) and a group's sum is fp32.
+ * with fp32 sums over the groups.  x' is off by at most 2^-22 of its group's largest
+ * |x'|, or 2^-128 (up to 4 tokens it is held in 22 bits below that; beyond 4 tokens bf16
+ * values are exact down to 2^-31 of it and x * cinv is off by at most 2^-22 of itself or
+ * 2^-39 of it).
  * A token with an x' beyond fp32's range gets infinities or NaN, the others are not
  * touched by it.
  *   x [M][K] bf16, 0 <= M <= 16; bias [N] fp32 or NULL; y [M][N] bf16 out;

@@ -1,0 +1,44 @@
+"""The group-scaled product where its value is decided by few bits: tokens and weights whose
+terms cancel, and values at the ends of the range.  Against 64-bit sums."""
+import pytest
+import torch
+
+from test_gpu_group import codes_of, gemv, packed
+
+pytestmark = pytest.mark.gpu
+
+
+def in_64_bits(x, cinv, qw, s_g, group):
+    """(y, sum of the terms' magnitudes, x', weights)."""
+    x8 = x.double() if cinv is None else x.double() * cinv.double()
+    w = torch.from_numpy(codes_of(qw.cpu().numpy())).cuda().double()
+    w = w * s_g.double().t().repeat_interleave(group, 1)
+    return x8 @ w.t(), x8.abs() @ w.abs().t(), x8, w
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,K", [(1, 512), (3, 512), (5, 512), (8, 2048), (9, 512), (16, 1024),
+                                 (12, 32768)])
+def test_scaled_tokens_keep_their_bits(M, K, group):
+    """Neighbouring channels with equal weights, opposite tokens and channel scales that
+    differ by 2^-13: what is left of their terms is in the low bits of x * cinv, which 11
+    bits do not have.  Allowed: half a bf16 step; x' off by 2^-22 of its group's largest (that
+    covers 2^-22 of itself); a group's sum in at most 16 matrix steps, each within 2^-22 of
+    the terms' magnitudes; the fp32 product of x and cinv, four operations to a group's term and
+    the additions over groups and parts, each 2^-24."""
+    g = torch.Generator(device="cuda").manual_seed(M * K + group)
+    N = 37
+    W = (torch.randn(N, K, generator=g, device="cuda") * 0.02).bfloat16()
+    W[:, 1::2] = W[:, 0::2]
+    qw, s_g = packed(W, None, group)
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    x[:, 1::2] = -x[:, 0::2]
+    cinv = torch.exp(torch.randn(K, generator=g, device="cuda") * 0.5)
+    cinv[1::2] = cinv[0::2] * (1 + 2.0 ** -13 * torch.rand(K // 2, generator=g, device="cuda"))
+    y = gemv(x, cinv, qw, s_g, group, None)
+    want, size, x8, w = in_64_bits(x, cinv, qw, s_g, group)
+    top = x8.abs().view(M, K // group, group).amax(-1).repeat_interleave(group, 1)
+    allow = want.abs() * 2.0 ** -8 + (top * 2.0 ** -22) @ w.abs().t() \
+        + size * ((K / group + 8 + 5) * 2.0 ** -24 + 16 * 2.0 ** -22) + 2.0 ** -133
+    off = (y.double() - want).abs()
+    assert bool((off <= allow).all()), float((off / allow).max())
