@@ -226,12 +226,70 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnMinUnits = 16;  // blocks of 16 tokens a CTA takes at least
 
-// Softmax weights enter the second product in f16 as 2^kPShift times their value
-// relative to a reference maximum that the running one may exceed by up to 2^kPSlack
-// before the sums are rescaled: at most 2^15 (f16 reaches 65504), full 11 bits down to
-// 2^-25 of the reference, and steps of 2^-35 of it below.  (8 bits of bf16 would do without
-// the shift, at eight times the rounding error; f32 weights cannot enter the instruction.)
+// Softmax weights p_j times the scale of their values' block enter the second product in f16,
+// as 2^kPShift times their value relative to a row's reference, which the largest of the row
+// so far may exceed by up to 2^kPSlack before the sums are rescaled: at most 2^15 (f16
+// reaches 65504), full 11 bits down to 2^-25 of the reference, and steps of 2^-35 of it below.
+// (8 bits of bf16 would do without the shift, at eight times the rounding error; f32 weights
+// cannot enter the instruction.)
 constexpr float kPShift = 11.0f, kPSlack = 4.0f;
+
+// 2^n for a whole n below 128, exactly; 0 below the subnormals.
+__device__ __forceinline__ float exp2_whole(float n) {
+  const int e = static_cast<int>(fmaxf(n, -150.0f));
+  return __uint_as_float(e >= -126 ? static_cast<uint32_t>(e + 127) << 23
+                                   : e >= -149 ? 1u << (e + 149) : 0u);
+}
+
+__device__ __forceinline__ float log2_approx(float x) {  // -infinity for subnormals
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A row's references: weights p_j = 2^(s_j - m), s_j the scores times log2(e); their products
+// with the value scales are held relative to 2^e.  Both exponents are whole, so that sums are
+// rescaled by powers of two.  e follows the row's own products: a block whose value scale is
+// large takes no bits from the others where the row gives it no weight.
+struct AttnRow {
+  float m, l;   // l: sum of 2^kPShift p_j
+  float bound;  // of s_j + log2(scale): m + e + kPSlack
+  float inv;    // 2^-e
+
+  __device__ __forceinline__ void start() {
+    m = bound = -INFINITY;
+    l = 0.0f;
+    inv = 0x1p125f;
+  }
+  // top: of scores, u: of scores + log2(value scale).  Any lane of a row may ask.
+  __device__ __forceinline__ bool exceeded(float top, float u) const {
+    return top > m + kPSlack || u > bound;
+  }
+  // The row's own top and u have come: the factor of its sums so far.
+  __device__ __forceinline__ float raise(float top, float u) {
+    const bool over = exceeded(top, u);
+    const float m_new = top > m + kPSlack ? ceilf(top) : m;
+    const float back = over ? m - m_new : 0.0f, e = exponent();
+    const float e_up = fminf(fmaxf(ceilf(fmaxf(u - m_new, e + back)), -125.0f), 126.0f);
+    const float e_new = over ? e_up : e;
+    l *= exp2_approx(back);
+    m = m_new;
+    bound = m_new + e_new + kPSlack;
+    inv = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(e_new)) << 23);
+    return exp2_approx(back + (e - e_new));
+  }
+  __device__ __forceinline__ float exponent() const {
+    return 127.0f - static_cast<float>(__float_as_uint(inv) >> 23);
+  }
+  // What turns p_j 2^kPShift into its f16 weight.  (Beyond 2^126 the weights are below 2^-122;
+  // an infinity would make a NaN of masked ones.)
+  __device__ __forceinline__ float weight(float sv) const {
+    float w;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(w) : "f"(sv * inv), "f"(0x1p126f));
+    return w;
+  }
+  __device__ __forceinline__ float base() const { return m == -INFINITY ? 0.0f : m - kPShift; }
+};
 
 struct AttnArgs {
   const uint16_t* q;      // bf16 rows [Tq], heads x D packed within a row
@@ -507,7 +565,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
 #pragma unroll
     for (int k = 0; k < WT; ++k) {
       const float mk = row_m[k][r];
-      if (mk != -INFINITY) sum += row_l[k][r] * exp2_approx(mk - top);
+      if (mk != -INFINITY) sum += row_l[k][r] * exp2_whole(mk - top);
       const float4 p = *reinterpret_cast<const float4*>(slabs[k] + slab_offset<D>(r - row0, d));
       v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
     }
@@ -669,15 +727,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
     for (int x = 16; x > 2; x >>= 1) see_min = min(see_min, __shfl_xor_sync(0xFFFFFFFFu, see_min, x));
 
     float o[MT][ND][4] = {};
-    float m[MT][2], l[MT][2];
+    AttnRow row[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        m[mt][h] = -INFINITY;
-        l[mt][h] = 0.0f;
-      }
-    float ref = 0.0f, inv_ref = 0.0f;  // power of two >= the value scales seen
+      for (int h = 0; h < 2; ++h) row[mt][h].start();
     int dead = -1;  // the step whose copies did not arrive in time
     for (int i = 0; i < count; ++i) {
       const uint32_t n = phase + i, st = n % STAGES;
@@ -722,15 +776,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
         }
       }
 
-      float sk[2], sv[2];
+      float sk[2], sv[2], log_sv[2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) seg.scales(i, c, sk[c], sv[c]);
+      for (int c = 0; c < 2; ++c) {
+        seg.scales(i, c, sk[c], sv[c]);
+        log_sv[c] = log2_approx(sv[c]);
+      }
       const int first = (j0 + 2 * (wt + WT * i)) * kBlockTokens;
       const int last = (j0 + blocks) * kBlockTokens;
       const bool cut = first + 2 * kBlockTokens > min(see_min, last);
-      const float sv_top = fmaxf(sv[0], sv[1]);
-      bool grow = sv_top > ref;
-      float top[MT][2], f[MT][2][2];  // f: from sums of products to scores, for each block
+      bool grow = false;
+      float top[MT][2], u[MT][2], f[MT][2][2];  // f: from sums of products to scores, for each block
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -753,31 +809,21 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
           for (int c = 0; c < 2; ++c)  // (no factor is negative)
             mx[c] = fmaxf(fmaxf(s[mt][2 * c][2 * h], s[mt][2 * c][2 * h + 1]),
                           fmaxf(s[mt][2 * c + 1][2 * h], s[mt][2 * c + 1][2 * h + 1])) * f[mt][h][c];
-          mx[0] = fmaxf(mx[0], mx[1]);
-          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], 1));
-          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], 2));
-          top[mt][h] = mx[0];
-          grow |= mx[0] > m[mt][h] + kPSlack;
+          top[mt][h] = fmaxf(mx[0], mx[1]);  // of my tokens; the row's only where it matters
+          u[mt][h] = fmaxf(mx[0] + log_sv[0], mx[1] + log_sv[1]);
+          grow |= row[mt][h].exceeded(top[mt][h], u[mt][h]);
         }
       if (__any_sync(0xFFFFFFFFu, grow)) {
-        float shrink = 1.0f;
-        if (sv_top > ref) {
-          const uint32_t e = max(min((__float_as_uint(sv_top) >> 23) + 1u, 252u), 2u);
-          inv_ref = __uint_as_float((254u - e) << 23);
-          shrink = ref * inv_ref;
-          ref = __uint_as_float(e << 23);
-        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float fade = 1.0f;
-            if (top[mt][h] > m[mt][h] + kPSlack) {
-              fade = exp2_approx(m[mt][h] - top[mt][h]);  // 0 for the first maximum
-              m[mt][h] = top[mt][h];
+#pragma unroll
+            for (int x = 1; x < 4; x *= 2) {
+              top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xFFFFFFFFu, top[mt][h], x));
+              u[mt][h] = fmaxf(u[mt][h], __shfl_xor_sync(0xFFFFFFFFu, u[mt][h], x));
             }
-            l[mt][h] *= fade;
-            fade *= shrink;
+            const float fade = row[mt][h].raise(top[mt][h], u[mt][h]);
 #pragma unroll
             for (int nd = 0; nd < ND; ++nd) {
               o[mt][nd][2 * h] *= fade;
@@ -790,13 +836,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float base = m[mt][h] == -INFINITY ? 0.0f : m[mt][h] - kPShift;
+          const float base = row[mt][h].base();
+          const float wvs[2] = {row[mt][h].weight(sv[0]), row[mt][h].weight(sv[1])};
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt) {
-            const float wv = sv[nt >> 1] * inv_ref;
+            const float wv = wvs[nt >> 1];
             const float p0 = exp2_approx(fmaf(s[mt][nt][2 * h], f[mt][h][nt >> 1], -base));
             const float p1 = exp2_approx(fmaf(s[mt][nt][2 * h + 1], f[mt][h][nt >> 1], -base));
-            l[mt][h] += p0 + p1;
+            row[mt][h].l += p0 + p1;
             pf[mt][nt >> 1][2 * (nt & 1) + h] = pack_half2(p0 * wv, p1 * wv);
           }
         }
@@ -854,11 +901,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        l[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][h], 1);
-        l[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][h], 2);
+        float l = row[mt][h].l;
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
         if (t == 0) {
-          row_m[wt][16 * mt + 8 * h + g] = m[mt][h];
-          row_l[wt][16 * mt + 8 * h + g] = l[mt][h];
+          row_m[wt][16 * mt + 8 * h + g] = row[mt][h].m;
+          row_l[wt][16 * mt + 8 * h + g] = l;
         }
       }
     // on to the next segment: its first copies go to the stage `phase` names, this one's sums
@@ -876,16 +924,18 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
       __syncthreads();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = 8 * h + g;
+        const int r = 8 * h + g;
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < WT; ++i) top = fmaxf(top, row_m[i][16 * mt + row]);
-        const float fade = m[mt][h] == -INFINITY ? 0.0f : exp2_approx(m[mt][h] - top) * ref;
+        for (int i = 0; i < WT; ++i) top = fmaxf(top, row_m[i][16 * mt + r]);
+        const AttnRow& mine = row[mt][h];
+        const float fade =
+            mine.m == -INFINITY ? 0.0f : exp2_whole(mine.m - top + mine.exponent());
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int nd = 0; nd < ND; nd += 4)
-            *reinterpret_cast<float4*>(slab + slab_offset<D>(row, t * (D / 4) + part * ND + nd)) =
+            *reinterpret_cast<float4*>(slab + slab_offset<D>(r, t * (D / 4) + part * ND + nd)) =
                 make_float4(o[mt][nd][2 * h + part] * fade, o[mt][nd + 1][2 * h + part] * fade,
                             o[mt][nd + 2][2 * h + part] * fade, o[mt][nd + 3][2 * h + part] * fade);
       }
@@ -1037,8 +1087,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
     }
 
     float o[MD][4] = {};  // channels (D / 8) g + 2 i and + 1, queries 2t and 2t + 1
-    float m = -INFINITY, l = 0.0f;
-    float ref = 0.0f, inv_ref = 0.0f;  // power of two >= the value scales seen
+    AttnRow row;
+    row.start();
     int dead = -1;  // the step whose copies did not arrive in time
     for (int i = 0; i < count; ++i) {
       const uint32_t n = phase + i, st = n % STAGES;
@@ -1093,42 +1143,36 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
               s[c][nt][e] = first + 16 * c + 8 * nt + 2 * t + e >= end ? -INFINITY : s[c][nt][e] * f[c];
         f[0] = f[1] = 1.0f;
       }
-      float top = fmaxf(fmaxf(fmaxf(s[0][0][0], s[0][0][1]), fmaxf(s[0][1][0], s[0][1][1])) * f[0],
-                        fmaxf(fmaxf(s[1][0][0], s[1][0][1]), fmaxf(s[1][1][0], s[1][1][1])) * f[1]);
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const float sv_top = fmaxf(sv[0], sv[1]);
-      if (__any_sync(0xFFFFFFFFu, sv_top > ref || top > m + kPSlack)) {
-        float shrink = 1.0f;
-        if (sv_top > ref) {
-          const uint32_t e = max(min((__float_as_uint(sv_top) >> 23) + 1u, 252u), 2u);
-          inv_ref = __uint_as_float((254u - e) << 23);
-          shrink = ref * inv_ref;
-          ref = __uint_as_float(e << 23);
+      float mx[2];  // of my tokens; the row's only where it matters
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        mx[c] = fmaxf(fmaxf(s[c][0][0], s[c][0][1]), fmaxf(s[c][1][0], s[c][1][1])) * f[c];
+      float top = fmaxf(mx[0], mx[1]);
+      float u = fmaxf(mx[0] + log2_approx(sv[0]), mx[1] + log2_approx(sv[1]));
+      if (__any_sync(0xFFFFFFFFu, row.exceeded(top, u))) {
+#pragma unroll
+        for (int x = 1; x < 4; x *= 2) {
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+          u = fmaxf(u, __shfl_xor_sync(0xFFFFFFFFu, u, x));
         }
-        float fade = 1.0f;
-        if (top > m + kPSlack) {
-          fade = exp2_approx(m - top);  // 0 for the first maximum
-          m = top;
-        }
-        l *= fade;
-        const float f0 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t) * shrink;
-        const float f1 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4) * shrink;
+        const float fade = row.raise(top, u);
+        const float f0 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t);
+        const float f1 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4);
 #pragma unroll
         for (int x = 0; x < MD; ++x) {
           o[x][0] *= f0; o[x][1] *= f1; o[x][2] *= f0; o[x][3] *= f1;
         }
       }
-      const float base = m == -INFINITY ? 0.0f : m - kPShift;
+      const float base = row.base();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float wv = sv[c] * inv_ref;
+        const float wv = row.weight(sv[c]);
         uint32_t pf[2];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           const float p0 = exp2_approx(fmaf(s[c][nt][0], f[c], -base));
           const float p1 = exp2_approx(fmaf(s[c][nt][1], f[c], -base));
-          l += p0 + p1;
+          row.l += p0 + p1;
           pf[nt] = pack_half2(p0 * wv, p1 * wv);
         }
         // values: lane (g, t) takes 16 (8) channels of tokens 2t, 2t+1, 2t+8, 2t+9
@@ -1170,10 +1214,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
         mbar_wait_drain(&full[wt][(phase + i) % STAGES], ((phase + i) / STAGES) & 1);
     phase += count;
 
+    float l = row.l;
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
     if (t == 0 && g < RT) {
-      row_m[wt][g] = m;
+      row_m[wt][g] = row.m;
       row_l[wt][g] = l;
     }
     // on to the next segment: its first copies go to the stage `phase` names, this one's
@@ -1189,7 +1234,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
     float top = -INFINITY;
 #pragma unroll
     for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k][FOUR ? g & 3 : g]);
-    const float fade = m == -INFINITY ? 0.0f : exp2_approx(m - top) * ref;
+    const float fade = row.m == -INFINITY ? 0.0f : exp2_whole(row.m - top + row.exponent());
     const float fq[2] = {__shfl_sync(0xFFFFFFFFu, fade, 8 * t), __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4)};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {

@@ -1,0 +1,87 @@
+"""Attention over the int8 cache where its value is decided by few bits or by the ends of the
+range: value scales, queries, weights and tables that the sums in 64 bits see and a rounding at
+the wrong place does not.  Every test runs in each tile height: 4, 8, 16 and 32 query rows."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_kv8 import BLOCK, attend, ints, page_table, random_cache, whole
+
+pytestmark = pytest.mark.gpu
+
+# queries, query heads, cache heads: rows of a tile 4, 8, 16, 32
+HEIGHTS = [(1, 2, 1), (1, 8, 1), (4, 4, 1), (8, 4, 1), (33, 2, 2)]
+
+
+def scales_of(cache, t, table, j):
+    """View of the scales [heads] of a sequence's block j."""
+    page = cache[t + "_codes"].shape[2]
+    return cache[t + "_scale"][int(table[j * BLOCK // page]), :, j * BLOCK % page // BLOCK]
+
+
+def codes_of(cache, t, table, j):
+    page = cache[t + "_codes"].shape[2]
+    at = j * BLOCK % page
+    return cache[t + "_codes"][int(table[j * BLOCK // page]), :, at:at + BLOCK]
+
+
+def in_64_bits(q, n, table, cache, causal, scale):
+    """(weights p [m][heads][n], scores, values [heads][n][D], sizes of the scores) of one
+    sequence, for every query head."""
+    Hq, Hkv = q.shape[1], cache["k_codes"].shape[1]
+    k = whole(cache["k_codes"], cache["k_scale"], table, n).repeat_interleave(Hq // Hkv, 0)
+    v = whole(cache["v_codes"], cache["v_scale"], table, n).repeat_interleave(Hq // Hkv, 0)
+    s = torch.einsum("mhd,hnd->mhn", q.double(), k) * scale
+    size = torch.einsum("mhd,hnd->mhn", q.double().abs(), k.abs()) * abs(scale)
+    if causal:
+        m = q.shape[0]
+        hidden = torch.arange(n, device="cuda")[None] > \
+            n - m + torch.arange(m, device="cuda")[:, None]
+        s = s.masked_fill(hidden[:, None], -math.inf)
+        size = size.masked_fill(hidden[:, None], 0)
+    top = s.amax(-1, keepdim=True)
+    p = torch.exp(s - top.masked_fill(top == -math.inf, 0))
+    return p / p.sum(-1, keepdim=True).clamp(min=1e-300), s, v, size
+
+
+def check(out, want, spread, held, relative):
+    """out within half a bf16 step of want, `relative` of spread = sum p|v| and `held`."""
+    allow = want.abs() * 2.0 ** -8 + spread * relative + held
+    off = (out.double() - want).abs()
+    assert bool((off <= allow).all()), float((off / allow).max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m,Hq,Hkv", HEIGHTS)
+@pytest.mark.parametrize("far", [0, 1, 9, 70])
+@pytest.mark.parametrize("causal", [False, True])
+def test_a_block_without_weight_takes_no_bits(causal, far, m, Hq, Hkv, D):
+    """Block `far` has a value scale 2^45 above the others' and scores that leave it no weight
+    (or, causal, the last token lies behind what the earlier queries see and has it): the
+    other blocks' values come out as if it were not there.  Allowed: weights of 11 bits,
+    2^-36 of the row's largest p * scale * 127 for each token, scores off by 2^-22 of their size
+    in (D / 16 + 8) steps, sums over the blocks in fp32."""
+    n, page, scale = 1200, 32, 0.125
+    table, pages = page_table([n], page, seed=far)
+    cache = random_cache(pages, Hkv, page, D, far + D)
+    g = torch.Generator(device="cuda").manual_seed(far + m)
+    q = torch.randn(m, Hq, D, generator=g, device="cuda").bfloat16()
+    q[..., 0] = 4.0
+    for j in range(-(-n // BLOCK)):
+        codes_of(cache, "k", table[0], j)[..., 0] = 0
+    last = -(-n // BLOCK) - 1
+    far = last if causal else far
+    scales_of(cache, "v", table[0], far).mul_(2.0 ** 45)
+    if not causal:
+        codes_of(cache, "k", table[0], far)[..., 0] = -127
+        scales_of(cache, "k", table[0], far).fill_(4.0)
+        codes_of(cache, "k", table[0], far)[..., 1:] = 0
+    out, _ = attend(q, ints([0, m]), ints([n]), table, cache, causal, scale)
+    p, s, v, size = in_64_bits(q, n, table[0], cache, causal, scale)
+    spread = torch.einsum("mhn,hnd->mhd", p, v.abs())
+    block_max = v.abs().amax(-1).view(Hq, -1, BLOCK).amax(-1).repeat_interleave(BLOCK, 1)
+    held = (p * block_max).amax(-1, keepdim=True) * n * 2.0 ** -36
+    steps = float(size.max() + 1) * (D / 16 + 8) * 2.0 ** -22
+    check(out, torch.einsum("mhn,hnd->mhd", p, v), spread, held,
+          2.0 ** -11 + 2 * steps + (n / BLOCK + 32) * 2.0 ** -22)
