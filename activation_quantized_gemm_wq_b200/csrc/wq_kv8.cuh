@@ -956,12 +956,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
 // Tiles of at most eight query rows (decoding with up to eight query heads to a cache
 // head): the same work in fewer instructions, which is what bounds it.
 // Scores come from the integer matrix instructions, with the cached codes as they are: q
-// becomes 22-bit integers relative to its row's largest value (off by at most 2^-22 of
-// it), three signed bytes hi, mid, lo.  For RT = 8, rows 0 to 7 of one operand are hi, 8 to
-// 15 mid, so that a lane holds both sums, and a second operand has lo; for RT = 4, one
-// operand has hi (rows 0 to 3), mid (4 to 7) and lo (8 to 11), and mid is fetched from
-// another lane.  Sums over the channels are exact.  A lane then holds the scores of row g for
-// tokens 2t, 2t + 1, which is the layout that the transposed product o^T += v^T p^T wants
+// becomes 30-bit integers relative to its row's largest value (off by at most 2^-30 of it,
+// and exact from 2^-21 of it on), four signed bytes.  For RT = 8, rows 0 to 7 of one operand
+// are the highest byte, 8 to 15 the next, so that a lane holds both sums, and a second operand
+// has the other two; for RT = 4, one operand has them all (rows 0 to 3 the highest, 8 to 11 the
+// third, 4 to 7 the second, 12 to 15 the lowest), and a row's two lanes exchange their halves.
+// Sums over the channels are exact and joined in fp32.  A lane then holds the scores of row g
+// (RT = 4: g modulo 4) for tokens 2t, 2t + 1, which is the layout that the transposed product o^T += v^T p^T wants
 // of p^T: half the instructions and accumulators of o += p v, of whose sixteen rows eight
 // would be empty.
 // A step is two blocks (32 tokens): the maxima, the reference and the barrier are looked
@@ -1042,7 +1043,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
 
     // its q as digits; channel 32t + 8s + 0..7 (D = 128; 16t + 8s for D = 64) of a row is
     // what lane t holds of a key for matrix step s
-    uint32_t qa[KS][4], ql[FOUR ? 1 : KS][2];  // RT = 8: hi, mid, hi, mid; lo, lo
+    uint32_t qa[KS][4], ql[FOUR ? 1 : KS][4];  // RT = 8: bytes 3, 2, 3, 2; 1, 0, 1, 0
     float qs;                                  // undoes the power-of-two scaling, times the softmax scale
     {
       uint4 raw[KS];
@@ -1061,10 +1062,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
       }
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const uint32_t ex = max(__float_as_uint(top) >> 23, 21u);
-      // 2^(21 - E), 2^E <= top < 2^(E + 1), with the softmax scale's sign
-      const float up = copysignf(__uint_as_float((275u - ex) << 23), a.scale_log2);
-      qs = FOUR && g >= 4 ? 0.0f : __uint_as_float((ex - 20u) << 23) * 0.5f * fabsf(a.scale_log2);
+      const uint32_t ex = max(__float_as_uint(top) >> 23, 29u);
+      // 2^(29 - E), 2^E <= top < 2^(E + 1), with the softmax scale's sign
+      const float up = copysignf(__uint_as_float((283u - ex) << 23), a.scale_log2);
+      qs = __uint_as_float((ex - 28u) << 23) * 0.5f * fabsf(a.scale_log2);
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -1072,16 +1073,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float v = (e & 1 ? bf16hi(w[e >> 1]) : bf16lo(w[e >> 1])) * up;
-          d[e] = (__float_as_uint(__fadd_rn(v, kRoundMagic)) - (0x4B400000u - 0x00808080u)) ^ 0x00808080u;
+          d[e] = (static_cast<uint32_t>(__float2int_rn(v)) + 0x00808080u) ^ 0x00808080u;
         }
+        const uint32_t upper = FOUR && g >= 4 ? 2u : 3u;  // (RT = 4: bytes 3, 1 or 2, 0)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t hi = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 2);
-          const uint32_t mid = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 1);
-          const uint32_t low = gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], 0);
-          qa[i][2 * h] = FOUR && g >= 4 ? mid : hi;
-          qa[i][2 * h + 1] = FOUR ? low : mid;
-          if constexpr (!FOUR) ql[i][h] = low;
+          auto bytes = [&](uint32_t byte) {
+            return gather_bytes(d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3], byte);
+          };
+          qa[i][2 * h] = bytes(upper);
+          qa[i][2 * h + 1] = bytes(FOUR ? upper - 2 : 2);
+          if constexpr (!FOUR) {
+            ql[i][2 * h] = bytes(1);
+            ql[i][2 * h + 1] = bytes(0);
+          }
         }
       }
     }
@@ -1116,18 +1121,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
             mma_s8(hm, qa[2 * x], kv.x, kv.y, x == 0);
             mma_s8(hm, qa[2 * x + 1], kv.z, kv.w, false);
             if constexpr (!FOUR) {
-              const uint32_t la[4] = {ql[2 * x][0], 0u, ql[2 * x][1], 0u};
-              const uint32_t lb[4] = {ql[2 * x + 1][0], 0u, ql[2 * x + 1][1], 0u};
-              mma_s8(lo, la, kv.x, kv.y, x == 0);
-              mma_s8(lo, lb, kv.z, kv.w, false);
+              mma_s8(lo, ql[2 * x], kv.x, kv.y, x == 0);
+              mma_s8(lo, ql[2 * x + 1], kv.z, kv.w, false);
             }
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int mid = FOUR ? __shfl_xor_sync(0xFFFFFFFFu, hm[e], 16) : hm[2 + e];
-            const int low = FOUR ? hm[2 + e] : lo[e];
-            s[c][nt][e] = fmaf(static_cast<float>(hm[e]), 65536.0f,
-                               static_cast<float>(mid * 256 + low));
+            if constexpr (FOUR) {
+              const float half = fmaf(static_cast<float>(hm[e]), 65536.0f,
+                                      static_cast<float>(hm[2 + e])) * (g < 4 ? 256.0f : 1.0f);
+              s[c][nt][e] = half + __shfl_xor_sync(0xFFFFFFFFu, half, 16);
+            } else {
+              s[c][nt][e] = fmaf(static_cast<float>(hm[e] * 256 + hm[2 + e]), 65536.0f,
+                                 static_cast<float>(lo[e] * 256 + lo[2 + e]));
+            }
           }
         }
       }

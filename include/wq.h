@@ -434,7 +434,8 @@ size_t wq_attn_kv8_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int
  *   q_start [B+1], kv_len [B] int32; out [Tq][q_heads][head_dim] bf16, rows outside every
  *   sequence are left as they were; lse [Tq][q_heads] fp32 or NULL: log of the sum of
  *   p_j, with which results over several caches can be joined.
- * Scores, softmax and sums are fp32; q keeps all its bits, the softmax weights are
+ * Scores, softmax and sums are fp32; values of q below 2^-21 of their row's largest (one
+ * query, one head) are off by at most 2^-30 of it, the others exact; the softmax weights are
  * rounded to 11 bits for the product with the codes.  For the same arguments the result
  * is the same on every call; calls that may run at the same time need workspaces of
  * their own.  Work is shared out from kv_len and q_start as they are on the device, so a

@@ -85,3 +85,29 @@ def test_a_block_without_weight_takes_no_bits(causal, far, m, Hq, Hkv, D):
     steps = float(size.max() + 1) * (D / 16 + 8) * 2.0 ** -22
     check(out, torch.einsum("mhn,hnd->mhd", p, v), spread, held,
           2.0 ** -11 + 2 * steps + (n / BLOCK + 32) * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m,Hq,Hkv", HEIGHTS)
+@pytest.mark.parametrize("n", [1, 40])
+def test_small_values_of_a_query_beside_a_large_one(n, m, Hq, Hkv, D):
+    """One channel of q is 2^13, and its key codes are 0: the scores are those of the other
+    channels.  Allowed: values below 2^-21 of the row's largest off by 2^-30 of it; the sum of
+    digits or of (D / 16 + 8) steps in fp32, 2^-22 of the terms' sizes each; the logarithm's
+    result, 2^-22 of it."""
+    page, scale = 16, 0.125
+    table, pages = page_table([n], page)
+    cache = random_cache(pages, Hkv, page, D, n + D)
+    cache["k_codes"][..., 5] = 0
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    q = torch.randn(m, Hq, D, generator=g, device="cuda").bfloat16()
+    q[..., 5] = 8192.0
+    _, lse = attend(q, ints([0, m]), ints([n]), table, cache, False, scale)
+    _, s, _, size = in_64_bits(q, n, table[0], cache, False, scale)
+    k = whole(cache["k_codes"], cache["k_scale"], table[0], n).repeat_interleave(Hq // Hkv, 0)
+    small = (q.double().abs() < 2.0 ** -8).double() * 2.0 ** -17
+    held = torch.einsum("mhd,hnd->mhn", small, k.abs()).amax(-1) * scale
+    want = torch.logsumexp(s, -1)
+    allow = held + (size.amax(-1) + 1) * (D / 16 + 8) * 2.0 ** -22 + want.abs() * 2.0 ** -22
+    off = (lse.double() - want).abs()
+    assert bool((off <= allow).all()), float((off / allow).max())
