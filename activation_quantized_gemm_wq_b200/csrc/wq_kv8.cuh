@@ -226,13 +226,20 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnMinUnits = 16;  // blocks of 16 tokens a CTA takes at least
 
-// Softmax weights p_j times the scale of their values' block enter the second product in f16,
-// as 2^kPShift times their value relative to a row's reference, which the largest of the row
-// so far may exceed by up to 2^kPSlack before the sums are rescaled: at most 2^15 (f16
-// reaches 65504), full 11 bits down to 2^-25 of the reference, and steps of 2^-35 of it below.
-// (8 bits of bf16 would do without the shift, at eight times the rounding error; f32 weights
-// cannot enter the instruction.)
+// Softmax weights p_j times the scale of their values' block enter the second product as two
+// f16 parts, the second what the first leaves over, multiplied by the same codes into the same
+// sums: one part alone would round them to 11 bits, which is seen where values cancel, and fp32
+// weights cannot enter the instruction.  They are 2^kPShift times their value relative to a
+// row's reference, which the largest of the row so far may exceed by up to 2^kPSlack before the
+// sums are rescaled: at most 2^15 (f16 reaches 65504), off by at most 2^-22 of themselves or
+// 2^-36 of the reference.
 constexpr float kPShift = 11.0f, kPSlack = 4.0f;
+
+// What two f16 leave over of two fp32 values, as f16.
+__device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t h) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_half2(a - f.x, b - f.y);
+}
 
 // 2^n for a whole n below 128, exactly; 0 below the subnormals.
 __device__ __forceinline__ float exp2_whole(float n) {
@@ -831,7 +838,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
             }
           }
       }
-      uint32_t pf[MT][2][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -844,7 +850,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
             const float p0 = exp2_approx(fmaf(s[mt][nt][2 * h], f[mt][h][nt >> 1], -base));
             const float p1 = exp2_approx(fmaf(s[mt][nt][2 * h + 1], f[mt][h][nt >> 1], -base));
             row[mt][h].l += p0 + p1;
-            pf[mt][nt >> 1][2 * (nt & 1) + h] = pack_half2(p0 * wv, p1 * wv);
+            s[mt][nt][2 * h] = p0 * wv;  // from scores to weights
+            s[mt][nt][2 * h + 1] = p1 * wv;
           }
         }
       // o += p v.  Lane (g, t) takes 16 (8) channels of tokens 2t, 2t+1, 2t+8, 2t+9; 4 x 4
@@ -864,25 +871,35 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
             vw[k][0] = v.x; vw[k][1] = v.y;
           }
         }
+        uint32_t pf[2][MT][4];  // the weights' two parts
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* w = &s[mt][2 * c + (k >> 1)][2 * (k & 1)];
+            pf[0][mt][k] = pack_half2(w[0], w[1]);
+            pf[1][mt][k] = half2_rest(w[0], w[1], pf[0][mt][k]);
+          }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
           uint32_t v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = vw[k][w] ^ 0x80808080u;
+          uint32_t f[4][2];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t x0 = __byte_perm(v[0], v[1], half ? 0x7362 : 0x5140);
-            const uint32_t x1 = __byte_perm(v[2], v[3], half ? 0x7362 : 0x5140);
+          for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t b0 = bytes_f16x2(x0, e ? 0x4342 : 0x4140);
-              const uint32_t b1 = bytes_f16x2(x1, e ? 0x4342 : 0x4140);
+            for (int k = 0; k < 2; ++k)
+              f[x][k] = bytes_f16x2(__byte_perm(v[2 * k], v[2 * k + 1], x >> 1 ? 0x7362 : 0x5140),
+                                    x & 1 ? 0x4342 : 0x4140);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)  // (a sum's two steps lie apart)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
-                mma_f16(o[mt][4 * w + 2 * half + e], pf[mt][c][0], pf[mt][c][1], pf[mt][c][2],
-                        pf[mt][c][3], b0, b1);
-            }
-          }
+                mma_f16(o[mt][4 * w + x], pf[part][mt][0], pf[part][mt][1], pf[part][mt][2],
+                        pf[part][mt][3], f[x][0], f[x][1]);
         }
       }
       __syncwarp();  // the stage has been read
@@ -962,9 +979,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
 // has the other two; for RT = 4, one operand has them all (rows 0 to 3 the highest, 8 to 11 the
 // third, 4 to 7 the second, 12 to 15 the lowest), and a row's two lanes exchange their halves.
 // Sums over the channels are exact and joined in fp32.  A lane then holds the scores of row g
-// (RT = 4: g modulo 4) for tokens 2t, 2t + 1, which is the layout that the transposed product o^T += v^T p^T wants
-// of p^T: half the instructions and accumulators of o += p v, of whose sixteen rows eight
-// would be empty.
+// (RT = 4: g modulo 4) for tokens 2t, 2t + 1, which is the layout that the transposed product
+// o^T += v^T p^T wants of p^T: half the instructions and accumulators of o += p v, of whose
+// sixteen rows eight would be empty.  For RT = 4 columns 0 to 3 of p^T are the weights' first
+// parts and columns 4 to 7 the second ones, at no more matrix steps.
 // A step is two blocks (32 tokens): the maxima, the reference and the barrier are looked
 // at once for both.  The first step of the next segment is fetched while this one's sums
 // are joined (in the other stage of each warp's ring).
@@ -1091,7 +1109,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
       }
     }
 
-    float o[MD][4] = {};  // channels (D / 8) g + 2 i and + 1, queries 2t and 2t + 1
+    // channels (D / 8) g + 2 i and + 1, queries 2t and 2t + 1; RT = 4: queries modulo 4, from
+    // the weights' first parts (columns 0 to 3) and second ones
+    float o[MD][4] = {};
     AttnRow row;
     row.start();
     int dead = -1;  // the step whose copies did not arrive in time
@@ -1174,13 +1194,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float wv = row.weight(sv[c]);
-        uint32_t pf[2];
+        uint32_t pf[2], rest[2];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           const float p0 = exp2_approx(fmaf(s[c][nt][0], f[c], -base));
           const float p1 = exp2_approx(fmaf(s[c][nt][1], f[c], -base));
           row.l += p0 + p1;
-          pf[nt] = pack_half2(p0 * wv, p1 * wv);
+          const float w0 = p0 * wv, w1 = p1 * wv;
+          pf[nt] = pack_half2(w0, w1);
+          rest[nt] = half2_rest(w0, w1, pf[nt]);
+          if (FOUR && g >= 4) pf[nt] = rest[nt];
         }
         // values: lane (g, t) takes 16 (8) channels of tokens 2t, 2t+1, 2t+8, 2t+9
         uint32_t vw[4][D / 32];
@@ -1201,12 +1224,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
           uint32_t v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = vw[k][w] ^ 0x80808080u;
-          const uint32_t lo0 = __byte_perm(v[0], v[1], 0x5140), hi0 = __byte_perm(v[0], v[1], 0x7362);
-          const uint32_t lo1 = __byte_perm(v[2], v[3], 0x5140), hi1 = __byte_perm(v[2], v[3], 0x7362);
-          mma_f16(o[2 * w], bytes_f16x2(lo0, 0x4140), bytes_f16x2(lo0, 0x4342),
-                  bytes_f16x2(lo1, 0x4140), bytes_f16x2(lo1, 0x4342), pf[0], pf[1]);
-          mma_f16(o[2 * w + 1], bytes_f16x2(hi0, 0x4140), bytes_f16x2(hi0, 0x4342),
-                  bytes_f16x2(hi1, 0x4140), bytes_f16x2(hi1, 0x4342), pf[0], pf[1]);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t x0 = __byte_perm(v[0], v[1], half ? 0x7362 : 0x5140);
+            const uint32_t x1 = __byte_perm(v[2], v[3], half ? 0x7362 : 0x5140);
+            const uint32_t f0 = bytes_f16x2(x0, 0x4140), f1 = bytes_f16x2(x0, 0x4342);
+            const uint32_t f2 = bytes_f16x2(x1, 0x4140), f3 = bytes_f16x2(x1, 0x4342);
+            mma_f16(o[2 * w + half], f0, f1, f2, f3, pf[0], pf[1]);
+            if constexpr (!FOUR) mma_f16(o[2 * w + half], f0, f1, f2, f3, rest[0], rest[1]);
+          }
         }
       }
       __syncwarp();  // the stage has been read
@@ -1243,6 +1269,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
     for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k][FOUR ? g & 3 : g]);
     const float fade = row.m == -INFINITY ? 0.0f : exp2_whole(row.m - top + row.exponent());
     const float fq[2] = {__shfl_sync(0xFFFFFFFFu, fade, 8 * t), __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4)};
+    if constexpr (FOUR) {  // the two parts
+#pragma unroll
+      for (int x = 0; x < MD; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][e] += __shfl_xor_sync(0xFFFFFFFFu, o[x][e], 2);
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (2 * t + e >= RT) break;

@@ -435,8 +435,9 @@ size_t wq_attn_kv8_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int
  *   sequence are left as they were; lse [Tq][q_heads] fp32 or NULL: log of the sum of
  *   p_j, with which results over several caches can be joined.
  * Scores, softmax and sums are fp32; values of q below 2^-21 of their row's largest (one
- * query, one head) are off by at most 2^-30 of it, the others exact; the softmax weights are
- * rounded to 11 bits for the product with the codes.  For the same arguments the result
+ * query, one head) are off by at most 2^-30 of it, the others exact; the products of
+ * softmax weights and value scales are held to 2^-22 of themselves or 2^-35 of their row's
+ * largest.  For the same arguments the result
  * is the same on every call; calls that may run at the same time need workspaces of
  * their own.  Work is shared out from kv_len and q_start as they are on the device, so a
  * captured call may be replayed after they changed.

@@ -111,3 +111,28 @@ def test_small_values_of_a_query_beside_a_large_one(n, m, Hq, Hkv, D):
     allow = held + (size.amax(-1) + 1) * (D / 16 + 8) * 2.0 ** -22 + want.abs() * 2.0 ** -22
     off = (lse.double() - want).abs()
     assert bool((off <= allow).all()), float((off / allow).max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m,Hq,Hkv", HEIGHTS)
+@pytest.mark.parametrize("n", [2, 16, 24])
+def test_weights_of_values_that_cancel(n, m, Hq, Hkv, D):
+    """Neighbouring tokens have opposite values and keys that differ by a code: what is left is
+    the difference of weights about 2^-12 apart, which 11 bits do not have.  Allowed: weights
+    held to 2^-22 and their largest's 2^-35; scores off by 2^-22 of their size in (D / 16 + 8)
+    steps, twice (the weight and the sum that divides it); sums over the blocks in fp32."""
+    page, scale = 16, 0.125
+    table, pages = page_table([n], page)
+    cache = random_cache(pages, Hkv, page, D, n + D)
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    k, v = cache["k_codes"], cache["v_codes"]
+    k.clamp_(-126, 126)
+    step = torch.randint(-1, 2, k[:, :, 1::2].shape, generator=g, device="cuda", dtype=torch.int8)
+    k[:, :, 1::2] = k[:, :, 0::2] + step
+    v[:, :, 1::2] = -v[:, :, 0::2]
+    q = (torch.randn(m, Hq, D, generator=g, device="cuda") * 0.02).bfloat16()
+    out, _ = attend(q, ints([0, m]), ints([n]), table, cache, False, scale)
+    p, s, v8, size = in_64_bits(q, n, table[0], cache, False, scale)
+    steps = float(size.max() + 1) * (D / 16 + 8) * 2.0 ** -22
+    check(out, torch.einsum("mhn,hnd->mhd", p, v8), torch.einsum("mhn,hnd->mhd", p, v8.abs()), 0,
+          2.0 ** -22 + n * 2.0 ** -35 + 2 * steps + (n / BLOCK + 32) * 2.0 ** -22)
