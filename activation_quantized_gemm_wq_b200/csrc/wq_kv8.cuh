@@ -235,6 +235,11 @@ constexpr int kAttnMinUnits = 16;  // blocks of 16 tokens a CTA takes at least
 // 2^-36 of the reference.
 constexpr float kPShift = 11.0f, kPSlack = 4.0f;
 
+// The sums of p v that leave the matrix instructions' accumulators are held at 2^-14 of their
+// value: values near fp32's largest then do not overflow in a sum whose quotient is in range,
+// and what is lost at the other end is below half of bf16's smallest step.
+constexpr float kSumUnit = 0x1p-14f, kOutUnit = 0x1p25f;  // 2^kPShift / kSumUnit
+
 // What two f16 leave over of two fp32 values, as f16.
 __device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t h) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
@@ -552,7 +557,7 @@ __device__ __forceinline__ int slab_offset(int row, int d) {
 // order, and written as the result, or as a partial one where other CTAs have a part of the
 // item; rows [row0, row0 + ROWS) of a tile of RT.  In shared memory: row_m, row_l [warp][row]
 // maxima and sums of the warps' rows, slabs[warp] their outputs of these rows, already
-// relative to that maximum.
+// relative to that maximum and in units of 1 / kSumUnit.
 template <int D, int RT, int ROWS>
 __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw,
                                             const float (*row_m)[RT], const float (*row_l)[RT],
@@ -577,7 +582,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
       v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
     }
     if (whole) {
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = sum > 0.0f ? kOutUnit / sum : 0.0f;
       const int qi = (r_first + r) / G, qh = head * G + (r_first + r) % G;
       const long long at = static_cast<long long>(sw.q0 + qi) * a.q_heads + qh;
       const __nv_bfloat162 x0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
@@ -949,6 +954,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
         const float fade =
             mine.m == -INFINITY ? 0.0f : exp2_whole(mine.m - top + mine.exponent());
 #pragma unroll
+        for (int nd = 0; nd < ND; ++nd)  // (kSumUnit / 2^kPShift times fade may be below the range)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) o[mt][nd][2 * h + e] *= 1.0f / kOutUnit;
+#pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int nd = 0; nd < ND; nd += 4)
@@ -1276,6 +1285,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
         for (int e = 0; e < 4; ++e) o[x][e] += __shfl_xor_sync(0xFFFFFFFFu, o[x][e], 2);
     }
 #pragma unroll
+    for (int x = 0; x < MD; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[x][e] *= 1.0f / kOutUnit;  // (times fade may be below the range)
+#pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (2 * t + e >= RT) break;
 #pragma unroll
@@ -1354,7 +1367,7 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
       v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, o);
     }
     if (lane % lanes != 0 || base + static_cast<int>(threadIdx.x) / lanes >= end) continue;
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum > 0.0f ? kOutUnit / sum : 0.0f;
     const int qi = (cut.r_first + r) / G, qh = cut.head * G + (cut.r_first + r) % G;
     const long long at = static_cast<long long>(cut.q0 + qi) * a.q_heads + qh;
     const __nv_bfloat162 x0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);

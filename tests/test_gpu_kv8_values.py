@@ -136,3 +136,25 @@ def test_weights_of_values_that_cancel(n, m, Hq, Hkv, D):
     steps = float(size.max() + 1) * (D / 16 + 8) * 2.0 ** -22
     check(out, torch.einsum("mhn,hnd->mhd", p, v8), torch.einsum("mhn,hnd->mhd", p, v8.abs()), 0,
           2.0 ** -22 + n * 2.0 ** -35 + 2 * steps + (n / BLOCK + 32) * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m,Hq,Hkv", HEIGHTS)
+@pytest.mark.parametrize("n", [30, 3000])
+@pytest.mark.parametrize("size", [2.0 ** 119, 2.0 ** -124])
+def test_values_at_the_ends_of_the_range(size, n, m, Hq, Hkv, D):
+    """Values up to 1.2 * 2^126 and down to 2^-131: their means are in range.  Allowed: half a
+    bf16 step, 2^-22 of sum p|v| as for any other values (weights, scores, sums), and the
+    ends' own steps: 2^-134 for bf16, 2^-135 for sums of p v over each part of the tokens."""
+    page, scale = 64, 0.125
+    table, pages = page_table([n], page)
+    cache = random_cache(pages, Hkv, page, D, n + D)
+    cache["v_scale"].fill_(size)
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    q = torch.randn(m, Hq, D, generator=g, device="cuda").bfloat16()
+    out, _ = attend(q, ints([0, m]), ints([n]), table, cache, True, scale)
+    p, s, v8, sizes = in_64_bits(q, n, table[0], cache, True, scale)
+    steps = float(sizes.max() + 1) * (D / 16 + 8) * 2.0 ** -22
+    check(out, torch.einsum("mhn,hnd->mhd", p, v8), torch.einsum("mhn,hnd->mhd", p, v8.abs()),
+          2.0 ** -134 + n / BLOCK * 2.0 ** -135,
+          2.0 ** -22 + n * 2.0 ** -35 + 2 * steps + (n / BLOCK + 32) * 2.0 ** -22)
