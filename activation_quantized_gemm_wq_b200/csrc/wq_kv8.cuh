@@ -223,6 +223,15 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
                   : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
+// 2^(e - 127 - bits) times the softmax scale's size, for a row of queries whose largest value has
+// the exponent field e >= bits: what turns its sums into scores.  A NaN if that value is not
+// finite: digits do not hold one, nor does a maximum or an infinite weight pass it on, but
+// scores that are NaN make all of the row's results NaN (of a row that sees any token).
+__device__ __forceinline__ float row_factor(uint32_t e, uint32_t bits, float scale) {
+  return e == 255u ? __uint_as_float(0x7FC00000u)
+                   : __uint_as_float((e - bits + 1u) << 23) * 0.5f * fabsf(scale);
+}
+
 constexpr int kAttnWarps = 4;
 constexpr int kAttnMinUnits = 16;  // blocks of 16 tokens a CTA takes at least
 
@@ -576,8 +585,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
     float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
     for (int k = 0; k < WT; ++k) {
-      const float mk = row_m[k][r];
-      if (mk != -INFINITY) sum += row_l[k][r] * exp2_whole(mk - top);
+      sum += row_l[k][r] * exp2_whole(row_m[k][r] - top);  // (a warp without tokens: 0 * 0)
       const float4 p = *reinterpret_cast<const float4*>(slabs[k] + slab_offset<D>(r - row0, d));
       v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
     }
@@ -590,7 +598,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
       *reinterpret_cast<uint2*>(a.out + at * D + d) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
       if (a.lse && d == 0)
-        a.lse[at] = sum > 0.0f ? (top - kPShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        a.lse[at] = sum == 0.0f ? -INFINITY : (top - kPShift + log2f(sum)) * 0.69314718055994531f;
     } else {
       *reinterpret_cast<float4*>(dst + r * D + d) = v;
       if (d == 0) {
@@ -707,15 +715,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
           const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            top = fmaxf(top, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
+            top = max_or_nan(top, max_or_nan(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
         }
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         // the largest value of the row comes to lie in [2^14, 2^15)
         const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
         // (the softmax scale's sign goes to q: factors of scores are not negative)
         const float up = copysignf(__uint_as_float((268u - e) << 23), a.scale_log2);
-        qs[mt][h] = __uint_as_float((e - 14u) << 23) * fabsf(a.scale_log2);
+        qs[mt][h] = row_factor(e, 14u, a.scale_log2);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -1085,14 +1093,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          top = fmaxf(top, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
+          top = max_or_nan(top, max_or_nan(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
       }
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       const uint32_t ex = max(__float_as_uint(top) >> 23, 29u);
       // 2^(29 - E), 2^E <= top < 2^(E + 1), with the softmax scale's sign
       const float up = copysignf(__uint_as_float((283u - ex) << 23), a.scale_log2);
-      qs = __uint_as_float((ex - 28u) << 23) * 0.5f * fabsf(a.scale_log2);
+      qs = row_factor(ex, 29u, a.scale_log2);
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -1344,8 +1352,8 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
       const float* p = a.partial + (2LL * c + (c == c0 ? 1 : 0)) * size;
       const float2 ml = *reinterpret_cast<const float2*>(p + RT * D + 2 * r);
       const float4 x = *reinterpret_cast<const float4*>(p + r * D + d);
+      if (ml.y == 0.0f) continue;  // an empty part
       const float to = fmaxf(top, ml.x);
-      if (to == -INFINITY) continue;  // empty parts
       const float f = exp2_approx(top - to), e = exp2_approx(ml.x - to);
       sum = sum * f + ml.y * e;
       v.x = v.x * f + x.x * e; v.y = v.y * f + x.y * e;
@@ -1375,7 +1383,7 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
     *reinterpret_cast<uint2*>(a.out + at * D + d) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
     if (a.lse && d == 0)
-      a.lse[at] = sum > 0.0f ? (top - kPShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      a.lse[at] = sum == 0.0f ? -INFINITY : (top - kPShift + log2f(sum)) * 0.69314718055994531f;
   }
 }
 

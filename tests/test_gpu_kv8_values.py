@@ -158,3 +158,29 @@ def test_values_at_the_ends_of_the_range(size, n, m, Hq, Hkv, D):
     check(out, torch.einsum("mhn,hnd->mhd", p, v8), torch.einsum("mhn,hnd->mhd", p, v8.abs()),
           2.0 ** -134 + n / BLOCK * 2.0 ** -135,
           2.0 ** -22 + n * 2.0 ** -35 + 2 * steps + (n / BLOCK + 32) * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m,Hq,Hkv", HEIGHTS)
+@pytest.mark.parametrize("n", [3, 100, 5000])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_query_that_is_not_finite_is_seen(bad, n, m, Hq, Hkv, D):
+    """One value of one query and head is not finite, in a channel whose key codes are 0: all of
+    its results are NaN (zeros and -infinity if it sees no token), all others are as before."""
+    page, scale = 32, 0.125
+    table, pages = page_table([n], page)
+    cache = random_cache(pages, Hkv, page, D, n)
+    cache["k_codes"][..., 9] = 0
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    q = torch.randn(m, Hq, D, generator=g, device="cuda").bfloat16()
+    for i in {0, m - 1}:
+        x = q.clone()
+        calm = attend(x, ints([0, m]), ints([n]), table, cache, True, scale)
+        x[i, 1, 9] = bad
+        out, lse = attend(x, ints([0, m]), ints([n]), table, cache, True, scale)
+        if n - m + i >= 0:
+            assert bool(out[i, 1].isnan().all()) and bool(lse[i, 1].isnan())
+        else:
+            assert bool((out[i, 1] == 0).all()) and float(lse[i, 1]) == -math.inf
+        out[i, 1], lse[i, 1] = calm[0][i, 1], calm[1][i, 1]
+        assert torch.equal(out, calm[0]) and torch.equal(lse, calm[1])
