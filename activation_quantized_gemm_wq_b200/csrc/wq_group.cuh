@@ -242,6 +242,11 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
   return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
 }
 
+// The products' sums are held at 2^-12 of their value until bias and rounding: a group's sum of
+// x' * code may exceed the largest |x'| 2^10 times, which must not leave fp32's range before
+// the weights' scale brings it back.  (The other end has room: bf16's smallest step is 2^-133.)
+constexpr float kSumDown = 0x1p-12f, kSumUp = 0x1p12f;
+
 constexpr int kGemvWarps = 16;
 constexpr int kGemvMaxSplit = 8;            // CTAs that share K (a portable cluster)
 constexpr int kGemvMaxTiles = 512;          // row tiles of a cluster
@@ -524,12 +529,13 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
                            gather_bytes(d[2], d[6], d[3], d[7], b));
           }
         }
-        // 2^(E - BITS), and the digits' 1 / 16 of the codes; digits cannot hold an x' that
+        // 2^(E - BITS) * kSumDown, and the digits' 1 / 16 of the codes; digits cannot hold an x' that
         // left fp32's range, so their scale says it (f16 holds infinities itself)
         if (pc % (G / 8) == 0)
           xscale[pc / (G / 8) * TOKENS + m] =
-              !HALF && ex == 255u ? __uint_as_float(0x7FC00000u)
-                                  : __uint_as_float((ex - BITS + 1u) << 23) * (HALF ? 0.5f : 0.03125f);
+              !HALF && ex == 255u
+                  ? __uint_as_float(0x7FC00000u)
+                  : __uint_as_float((ex - BITS + 1u) << 23) * (kSumDown * (HALF ? 0.5f : 0.03125f));
       }
       if (base0 + XB * THREADS < pieces_all) fetch_x(base + XB * THREADS);
     }
@@ -702,7 +708,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) gemv_w4g_kernel(
       v = tile_sum(q / SEG, q % SEG);
     }
     a.y[static_cast<size_t>(m) * N + n] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(v + (a.bias ? a.bias[n] : 0.0f)));
+        __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(v, kSumUp, a.bias ? a.bias[n] : 0.0f)));
   }
   if (S > 1) cluster_sync();  // nobody leaves while its sums are read
 }

@@ -42,3 +42,30 @@ def test_scaled_tokens_keep_their_bits(M, K, group):
         + size * ((K / group + 8 + 5) * 2.0 ** -24 + 16 * 2.0 ** -22) + 2.0 ** -133
     off = (y.double() - want).abs()
     assert bool((off <= allow).all()), float((off / allow).max())
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("M", [1, 3, 5, 8, 9, 16])
+@pytest.mark.parametrize("size,weight", [(3e38, 2.0 ** -20), (3e38, 2.0 ** -100), (2.0 ** -60, 2.0 ** 100),
+                                         (2.0 ** -110, 2.0 ** 20), (2.0 ** -115, 0.25)])
+def test_tokens_and_scales_at_the_ends_of_the_range(size, weight, M, scaled, group):
+    """Tokens up to bf16's largest against small weight scales, and the other way round, with the
+    code -8, which packing never makes but a byte can hold: y is in range, and so is every sum
+    on the way.  Allowed as above, and at bf16's lower end 2^-133: half of its smallest step
+    and as much for the sums' own."""
+    K, N = 512, 24
+    g = torch.Generator(device="cuda").manual_seed(M + group)
+    qw = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    qw[:2] = 0x88                                          # -8 everywhere: the largest sums
+    s_g = ((torch.rand(K // group, N, generator=g, device="cuda") + 0.5) * weight).bfloat16()
+    x = (torch.rand(M, K, generator=g, device="cuda") * 0.75 + 0.25) * size
+    x = (x * torch.where(torch.rand(M, K, generator=g, device="cuda") < 0.3, -1.0, 1.0)).bfloat16()
+    cinv = torch.rand(K, generator=g, device="cuda") * 0.5 + 0.5 if scaled else None
+    y = gemv(x, cinv, qw, s_g, group, None)
+    want, sizes, x8, w = in_64_bits(x, cinv, qw, s_g, group)
+    top = x8.abs().view(M, K // group, group).amax(-1).repeat_interleave(group, 1)
+    allow = want.abs() * 2.0 ** -8 + (top * 2.0 ** -22 + 2.0 ** -128) @ w.abs().t() \
+        + sizes * ((K / group + 8 + 5) * 2.0 ** -24 + 16 * 2.0 ** -22) + 2.0 ** -133
+    off = (y.double() - want).abs()
+    assert bool((off <= allow).all()), float((off / allow).max())
