@@ -86,9 +86,13 @@ __global__ void __launch_bounds__(128, D == 128 ? 5 : 7) kv8_append_kernel(const
   const uint32_t windows = (a.T + a.window - 1) / a.window;
   griddep_wait();
   griddep_launch_dependents();
-  if (unit == 0)  // the table of rows as a whole, once
-    for (int i = lane; i < a.B; i += 32)
-      if (a.row_start[i] > a.row_start[i + 1]) raise_cache_error();
+  const long long capacity = static_cast<long long>(a.max_pages) * a.page_tokens;
+  if (unit == 0)  // the tables as a whole, once: a sequence may have no row that a warp looks at
+    for (int i = lane; i < a.B; i += 32) {
+      const long long lo = a.row_start[i], hi = a.row_start[i + 1], past = a.past_len[i];
+      if (lo < 0 || hi < lo || hi > a.T || past < 0 || past + (hi - lo) > capacity)
+        raise_cache_error();
+    }
   if (unit >= windows * a.heads * 2u) return;
   const int which = unit & 1;
   const int head = (unit >> 1) % static_cast<uint32_t>(a.heads);
@@ -98,7 +102,6 @@ __global__ void __launch_bounds__(128, D == 128 ? 5 : 7) kv8_append_kernel(const
   int8_t* codes = which ? a.codes[1] : a.codes[0];
   float* scales = which ? a.scale[1] : a.scale[0];
   const long long stride = which ? a.stride[1] : a.stride[0];
-  const long long capacity = static_cast<long long>(a.max_pages) * a.page_tokens;
 
   int t = max(t0, a.row_start[0]), b = -1;
   int first = 0, last = 0, past = 0;  // rows [first, last) of sequence b

@@ -1,0 +1,77 @@
+"""The int8 cache's device checks: every table that the header forbids is reported, whichever
+rows the calls' warps look at, and a good one is not."""
+import numpy as np
+import pytest
+import torch
+
+import activation_quantized_gemm_wq_b200 as wq
+from test_gpu_kv8 import append_reference, attend, ints, page_table, random_cache
+
+pytestmark = pytest.mark.gpu
+
+T, D, HEADS, PAGE, ROOM = 8, 64, 2, 16, 32      # rows, head size, heads, page and table sizes
+
+# row_start, past_len: 8 rows, room for 32 tokens in each sequence's table
+BAD = [([0, 8, 9], [0, 0]), ([9, 12], [0]), ([8, 9], [0]), ([-3, 0, 8], [0, 0]), ([-3, -1], [0]),
+       ([0, 8, 8], [0, -1]), ([0, 0, 8], [-5, 0]), ([8, 8], [-1]), ([0, 8, 8], [0, 33]),
+       ([0, 4, 2, 8], [0, 0, 0]), ([0, 8], [25]), ([0, 8, 2147483647], [0, 0]),
+       ([-2147483648, 0, 8], [0, 0]), ([0, 8], [2147483647]), ([0, 8, 8], [0, -2147483648])]
+GOOD = [([0, 8, 8], [0, 32]), ([0, 8], [24]), ([3, 3, 5], [32, 30]), ([8, 8], [0])]
+
+
+def append(starts, past):
+    table, pages = page_table([ROOM] * len(past), PAGE)
+    cache = random_cache(pages, HEADS, PAGE, D, 6)
+    before = {n: t.clone() for n, t in cache.items()}
+    x = torch.randn(T, HEADS, D, generator=torch.Generator(device="cuda").manual_seed(1),
+                    device="cuda").bfloat16()
+    wq.wq_kv8_append(x, x, ints(starts), ints(past), table, **cache)
+    return x, table, cache, before
+
+
+@pytest.mark.parametrize("starts,past", BAD)
+def test_append_reports_every_bad_table(starts, past):
+    """Reported, and a sequence whose rows lie within T and fit is written as if alone."""
+    x, table, cache, before = append(starts, past)
+    assert wq.wq_device_status() == ("WQ_ERR_DEVICE", 4)
+    if starts == sorted(starts):
+        want = {n: t.cpu().numpy().copy() for n, t in before.items()}
+        for b, p in enumerate(past):
+            lo, hi = starts[b:b + 2]
+            if lo < 0 or hi > T or p < 0 or p + hi - lo > ROOM:
+                continue
+            for t in ("k", "v"):
+                append_reference(x.float().cpu().numpy(), [lo, hi], [p], table[b:b + 1].cpu().numpy(),
+                                 want[t + "_codes"], want[t + "_scale"])
+        for n in want:
+            assert np.array_equal(cache[n].cpu().numpy(), want[n]), n
+
+
+@pytest.mark.parametrize("starts,past", GOOD)
+def test_append_reports_no_good_table(starts, past):
+    append(starts, past)
+    assert wq.wq_device_status() == ("WQ_OK", 0)
+
+
+def test_append_looks_at_every_one_of_many_sequences():
+    """The only bad entry is the last of 1000 sequences, without rows."""
+    n = 1000
+    table = torch.zeros(n, 2, dtype=torch.int32, device="cuda")
+    cache = random_cache(3, HEADS, PAGE, D, 6)
+    x = torch.randn(T, HEADS, D, device="cuda").bfloat16()
+    starts, past = [0] + [T] * n, [0] * n
+    wq.wq_kv8_append(x, x, ints(starts), ints(past), table, **cache)
+    assert wq.wq_device_status() == ("WQ_OK", 0)
+    past[-1] = -1
+    wq.wq_kv8_append(x, x, ints(starts), ints(past), table, **cache)
+    assert wq.wq_device_status() == ("WQ_ERR_DEVICE", 4)
+
+
+@pytest.mark.parametrize("starts,past", BAD)
+def test_attention_reports_every_bad_table(starts, past):
+    """The same tables as queries' rows and cached lengths."""
+    table, pages = page_table([ROOM] * len(past), PAGE)
+    cache = random_cache(pages, HEADS, PAGE, D, 6)
+    q = torch.randn(T, HEADS, D, device="cuda").bfloat16()
+    attend(q, ints(starts), ints([p + 8 if p == 25 else p for p in past]), table, cache, False, 0.1)
+    assert wq.wq_device_status() == ("WQ_ERR_DEVICE", 4)
