@@ -533,8 +533,9 @@ struct AttnSegment {
     const int slot = pos % a.page_tokens;
     row = static_cast<int>(hp * a.page_tokens + slot);
     const long long at = hp * (a.page_tokens / kBlockTokens) + slot / kBlockTokens;
-    sk = a.k_scale[at];
-    sv = a.v_scale[at];
+    // (an infinity becomes a NaN: a score of -infinity would pass for a masked one)
+    sk = fmaf(a.k_scale[at], 0.0f, a.k_scale[at]);
+    sv = fmaf(a.v_scale[at], 0.0f, a.v_scale[at]);
   }
 
   int b_;
@@ -808,6 +809,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
       const int first = (j0 + 2 * (wt + WT * i)) * kBlockTokens;
       const int last = (j0 + blocks) * kBlockTokens;
       const bool cut = first + 2 * kBlockTokens > min(see_min, last);
+      // a value scale that is not finite stays with the rows that see its block
+      const bool odd = cut && !(sv[0] + sv[1] < INFINITY);
       bool grow = false;
       float top[MT][2], u[MT][2], f[MT][2][2];  // f: from sums of products to scores, for each block
 #pragma unroll
@@ -859,7 +862,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float base = row[mt][h].base();
-          const float wvs[2] = {row[mt][h].weight(sv[0]), row[mt][h].weight(sv[1])};
+          float wvs[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            wvs[c] = row[mt][h].weight(sv[c]);
+            if (odd && first + 16 * c >= min(see[mt][h], last)) wvs[c] = 0.0f;
+          }
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt) {
             const float wv = wvs[nt >> 1];
@@ -1179,8 +1187,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
         }
       }
       const int first = (j0 + 2 * (wt + WT * i)) * kBlockTokens;
-      if (first + 2 * kBlockTokens > min(see_min, (j0 + blocks) * kBlockTokens)) {
-        const int end = min(see, (j0 + blocks) * kBlockTokens);
+      const int end = min(see, (j0 + blocks) * kBlockTokens);
+      const bool cut = first + 2 * kBlockTokens > min(see_min, (j0 + blocks) * kBlockTokens);
+      // a value scale that is not finite stays with the rows that see its block
+      const bool odd = cut && !(sv[0] + sv[1] < INFINITY);
+      if (cut) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -1213,7 +1224,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
       const float base = row.base();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float wv = row.weight(sv[c]);
+        float wv = row.weight(sv[c]);
+        if (odd && first + 16 * c >= end) wv = 0.0f;
         uint32_t pf[2], rest[2];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {

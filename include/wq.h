@@ -432,7 +432,8 @@ size_t wq_attn_kv8_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int
  * j <= kv_len[b] - n + i, n the sequence's number of queries: the queries are its last n
  * tokens.  A query that sees no token gets out = 0 and lse = -infinity.
  * A query (one row and head) with a value that is not finite gets NaN, if it sees any
- * token; the others are not touched by it.
+ * token; the others are not touched by it.  A block whose scale is not finite gives NaN
+ * to the queries that see a token of it, and to no other.
  *   q_start [B+1], kv_len [B] int32; out [Tq][q_heads][head_dim] bf16, rows outside every
  *   sequence are left as they were; lse [Tq][q_heads] fp32 or NULL: log of the sum of
  *   p_j, with which results over several caches can be joined.

@@ -184,3 +184,23 @@ def test_a_query_that_is_not_finite_is_seen(bad, n, m, Hq, Hkv, D):
             assert bool((out[i, 1] == 0).all()) and float(lse[i, 1]) == -math.inf
         out[i, 1], lse[i, 1] = calm[0][i, 1], calm[1][i, 1]
         assert torch.equal(out, calm[0]) and torch.equal(lse, calm[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m,Hq,Hkv", [(4, 1, 1), (8, 1, 1), (16, 1, 1), (20, 4, 1), (40, 2, 2)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("t", ["k", "v"])
+def test_scales_of_blocks_that_a_query_does_not_see(t, bad, m, Hq, Hkv, D):
+    """Causal, and the last block's scale is not finite: the queries that do not see it have what
+    they have without it, bit for bit; those that do are not finite."""
+    page, scale = 16, 0.125
+    for n in (33, 97, 417):                                # one token in the last block
+        table, pages = page_table([n], page)
+        cache = random_cache(pages, Hkv, page, D, n)
+        g = torch.Generator(device="cuda").manual_seed(m + n)
+        q = torch.randn(m, Hq, D, generator=g, device="cuda").bfloat16()
+        out, lse = attend(q, ints([0, m]), ints([n]), table, cache, True, scale)
+        scales_of(cache, t, table[0], n // BLOCK).fill_(bad)
+        bad_out, bad_lse = attend(q, ints([0, m]), ints([n]), table, cache, True, scale)
+        assert torch.equal(bad_out[:-1], out[:-1]) and torch.equal(bad_lse[:-1], lse[:-1])
+        assert not bool(bad_out[-1].isfinite().any())
