@@ -155,10 +155,13 @@ __global__ void __launch_bounds__(128, D == 128 ? 5 : 7) kv8_append_kernel(const
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
+        amax = max_or_nan(amax, max_or_nan(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
     }
-    amax = warp_max(amax);
-    const float s = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      amax = max_or_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    // (a maximum that is not finite gives NaN, and a block that has one keeps it)
+    const float s = max_or_nan(s_old, __fdiv_rn(fmaf(amax, 0.0f, amax), 127.0f));
     const bool plain = plain_scale(s);
     const float r = plain ? __frcp_rn(s) : 0.0f;
 #pragma unroll
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(128, D == 128 ? 5 : 7) kv8_append_kernel(const
         *p = pack_low_bytes(q[0], q[1], q[2], q[3]);
       }
     }
-    if (lane == 0 && (!in_block || s > s_old)) *sp = s;
+    if (lane == 0 && (!in_block || !(s <= s_old))) *sp = s;
     t = stop;
   }
 }

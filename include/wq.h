@@ -404,6 +404,8 @@ wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
  *                                        before past_len[b], else 0
  *   new code = clamp(rint_half_even(x / s_new), -127, 127), 0 where s_new is 0
  *   old code = rint_half_even(old code * (s_old / s_new))   where s_new > s_old
+ * (a value that is not finite makes s_new NaN, and a block with such a scale keeps it:
+ * its keys or values are not finite to the queries that see them)
  * in IEEE fp32: the scale is that of the largest value in the block, however the tokens
  * came; a token costs at most half a step when it is written and half a step each time
  * a later token of its block raises the scale.  Slots behind the new tokens keep their

@@ -75,3 +75,40 @@ def test_attention_reports_every_bad_table(starts, past):
     q = torch.randn(T, HEADS, D, device="cuda").bfloat16()
     attend(q, ints(starts), ints([p + 8 if p == 25 else p for p in past]), table, cache, False, 0.1)
     assert wq.wq_device_status() == ("WQ_ERR_DEVICE", 4)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("t", ["k", "v"])
+def test_append_of_a_value_that_is_not_finite_is_seen(t, bad, D):
+    """Its block of its head has a scale that is NaN, also after more tokens came to the block,
+    until a sequence begins it anew; the other blocks and heads, and of keys and values the
+    other one, are what they are without it."""
+    page, n, at = 32, 40, 21                               # token 21 lies in block 1
+    table, pages = page_table([64], page)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    x = {u: torch.randn(64, HEADS, D, generator=g, device="cuda").bfloat16() for u in "kv"}
+    y = {u: x[u].clone() for u in "kv"}
+    y[t][at, 1, 5] = bad
+    good, got = random_cache(pages, HEADS, page, D, 2), random_cache(pages, HEADS, page, D, 2)
+    for cache, rows in ((good, x), (got, y)):
+        for lo, hi in ((0, 18), (18, 30), (30, n)):        # block 1: begun, gone on with, ended
+            wq.wq_kv8_append(rows["k"][lo:hi], rows["v"][lo:hi], ints([0, hi - lo]), ints([lo]),
+                             table, **cache)
+    hit = int(table[0, 0])
+    assert bool(got[t + "_scale"][hit, 1, 1].isnan())
+    q = torch.randn(1, HEADS, D, device="cuda").bfloat16()
+    out, lse = attend(q, ints([0, 1]), ints([n]), table, got, True, 0.1)
+    want, want_lse = attend(q, ints([0, 1]), ints([n]), table, good, True, 0.1)
+    assert bool(out[0, 1].isnan().all()) and torch.equal(out[0, 0], want[0, 0])
+    assert bool(lse[0, 1].isnan()) == (t == "k") and torch.equal(lse[0, 0], want_lse[0, 0])
+    for u in "kv":
+        for kind in ("_codes", "_scale"):
+            a, b = got[u + kind].clone(), good[u + kind].clone()
+            if u == t:
+                blk = (hit, 1, slice(16, 32)) if kind == "_codes" else (hit, 1, 1)
+                a[blk], b[blk] = 0, 0
+            assert torch.equal(a, b), u + kind
+    wq.wq_kv8_append(x["k"][:n], x["v"][:n], ints([0, n]), ints([0]), table, **got)
+    assert bool(got[t + "_scale"][hit, 1, 1].isfinite())
+    assert wq.wq_device_status() == ("WQ_OK", 0)
