@@ -51,6 +51,13 @@ __device__ __forceinline__ void quantize8_pairs(const float2 (&v)[4], float s, f
 // not rounded to 0 is exact, and the scale, a maximum over QMAX, is within 2^-8 of that.
 __device__ __forceinline__ bool plain_scale(float s) { return s >= 0x1p-100f && s <= 0x1p120f; }
 
+// The larger one, or NaN if one is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // ------------------------------------------------------------ packing (offline)
 
 // Codes of eight channels (in the low nibbles) as one word of the packed layout.
@@ -132,10 +139,11 @@ __global__ void __launch_bounds__(256, 2) pack_int4_group_kernel(
           for (int e = 0; e < 4; ++e) v[j][e] = __fmul2_rn(v[j][e], cc[j0 + j][e]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(v[j][e].x), fabsf(v[j][e].y)));
+        for (int e = 0; e < 4; ++e)
+          amax = max_or_nan(amax, max_or_nan(fabsf(v[j][e].x), fabsf(v[j][e].y)));
       }
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      amax = max_or_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = max_or_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
       const float s = __bfloat162float(sb);
       const bool plain = plain_scale(s);
@@ -266,13 +274,6 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* desc, ui
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(desc)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
-}
-
-// The larger one, or NaN if one is.
-__device__ __forceinline__ float max_or_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
 }
 
 struct GemvArgs {

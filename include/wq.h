@@ -356,7 +356,8 @@ wq_status wq_linear_w4a8_noalloc(const wq_bf16* x, int M, int K, int N, const fl
  * W' = fp32(W) * c (c may be NULL, meaning 1),
  *   s_g[k/group][n] = bf16(max over the group of |W'[n,k]| / 7)
  *   code[n,k]       = clamp(rint_half_even(W'[n,k] / s_g), -7, 7), 0 where s_g is 0
- * with IEEE fp32 divisions; the codes are decided by the rounded scale.
+ * with IEEE fp32 divisions; the codes are decided by the rounded scale.  A group with a W'
+ * that is not finite gets a scale that is not: neither is any product with it.
  *   W [N][K] bf16; group 32, 64 or 128 (else WQ_ERR_ARG); 1 <= N <= 2^30;
  *   qw [N][K/2] uint8 out; s_g [K/group][N] bf16 out.
  * Layout of qw (not wq_pack_int4's): in each run of 128 channels (64 bytes, sixteen

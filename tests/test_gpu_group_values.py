@@ -69,3 +69,28 @@ def test_tokens_and_scales_at_the_ends_of_the_range(size, weight, M, scaled, gro
         + sizes * ((K / group + 8 + 5) * 2.0 ** -24 + 16 * 2.0 ** -22) + 2.0 ** -133
     off = (y.double() - want).abs()
     assert bool((off <= allow).all()), float((off / allow).max())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf"), 3e38])
+def test_a_weight_that_is_not_finite_is_seen(bad, group):
+    """One weight is not finite, or its product with the channel scale is not: its group's scale
+    says so, and so does every product of its row; all else is what it is without it."""
+    N, K, n, k = 21, 512, 13, 300
+    g = torch.Generator(device="cuda").manual_seed(group)
+    W = torch.randn(N, K, generator=g, device="cuda").bfloat16()
+    c = torch.full((K,), 4.0, device="cuda")
+    calm = packed(W, c, group)
+    W[n, k] = bad
+    qw, s_g = packed(W, c, group)
+    assert not bool(s_g[k // group, n].isfinite())
+    for M in (1, 3, 8, 16):
+        x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+        x[0] = 0
+        y, want = gemv(x, None, qw, s_g, group, None), gemv(x, None, *calm, group, None)
+        assert not bool(y[:, n].isfinite().any())
+        y[:, n] = want[:, n]
+        assert torch.equal(y, want)
+    run = slice(k // 128 * 64, k // 128 * 64 + 64)
+    qw[n, run], s_g[k // group, n] = calm[0][n, run], calm[1][k // group, n]
+    assert torch.equal(qw, calm[0]) and torch.equal(s_g, calm[1])
