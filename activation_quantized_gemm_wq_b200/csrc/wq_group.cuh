@@ -739,10 +739,10 @@ constexpr int gemv_tiles_limit(int share) {
 
 // Clusters of S CTAs, one CTA per SM, that run at the same time on the current device (a
 // GPU's SMs come in groups that larger clusters do not fill: 148, 74, 33 and 15 clusters
-// of 1, 2, 4 and 8 here).  Asked once per device.
+// of 1, 2, 4 and 8 here).  Asked once per device and instance of the kernel, whose table
+// `known` is (all instances have one type).
 template <class Kernel>
-int gemv_clusters(Kernel kernel, int S) {
-  static std::atomic<int> known[kAttrDevices][4];
+int gemv_clusters(Kernel kernel, std::atomic<int> (&known)[kAttrDevices][4], int S) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   const int at = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3;
@@ -762,7 +762,7 @@ int gemv_clusters(Kernel kernel, int S) {
   q.numAttrs = 1;
   if (cudaOccupancyMaxActiveClusters(&n, kernel, &q) != cudaSuccess || n < 1) {
     cudaGetLastError();
-    n = sm_count() / S > 0 ? sm_count() / S : 1;
+    return sm_count() / S > 0 ? sm_count() / S : 1;  // an estimate, not kept
   }
   if (cached) known[dev][at].store(n, std::memory_order_relaxed);
   return n;
@@ -774,6 +774,7 @@ cudaError_t run_gemv(const uint16_t* x, const float* cinv, const uint8_t* qw, co
   using Cfg = GemvCfg<MT, NT, TINY, TWO>;
   const int runs = K / 128, tiles = (N + Cfg::WR - 1) / Cfg::WR;
   static std::atomic<bool> done[kAttrDevices];
+  static std::atomic<int> known[kAttrDevices][4];
   const cudaError_t e = set_smem_once(gemv_w4g_kernel<G, MT, NT, TINY, TWO>, kGemvMaxSmem, done);
   if (e != cudaSuccess) return e;
   // The split of K, by what an SM has to do, in KB of weights: the tiles of its clusters,
@@ -785,7 +786,7 @@ cudaError_t run_gemv(const uint16_t* x, const float* cinv, const uint8_t* qw, co
     const int share = (runs + c - 1) / c;
     const int limit = gemv_tiles_limit<G, MT, NT, TINY, TWO>(share);
     if (limit < 1) continue;
-    const int clusters = gemv_clusters(gemv_w4g_kernel<G, MT, NT, TINY, TWO>, c);
+    const int clusters = gemv_clusters(gemv_w4g_kernel<G, MT, NT, TINY, TWO>, known, c);
     int take = (tiles + clusters - 1) / clusters;
     if (take > limit) take = limit;
     const long long waves = ((tiles + take - 1) / take + clusters - 1) / clusters;
