@@ -586,18 +586,13 @@ wq_status wq_attn_kv8(const wq_bf16* q, int64_t q_stride, int Tq, int q_heads,
 }
 
 wq_status wq_device_status(unsigned* flags) {
-  unsigned word = 0, cache_word = 0;
-  const unsigned zero = 0;
+  unsigned words[2] = {0, 0};
+  const unsigned zero[2] = {0, 0};
   if (cudaDeviceSynchronize() != cudaSuccess) return WQ_ERR_CUDA;
-  if (cudaMemcpyFromSymbol(&word, wq::g_error_word, sizeof word) != cudaSuccess) return WQ_ERR_CUDA;
-  if (word != 0 && cudaMemcpyToSymbol(wq::g_error_word, &zero, sizeof zero) != cudaSuccess)
+  if (cudaMemcpyFromSymbol(words, wq::g_error_words, sizeof words) != cudaSuccess) return WQ_ERR_CUDA;
+  const unsigned word = words[0] | words[1];
+  if (word != 0 && cudaMemcpyToSymbol(wq::g_error_words, zero, sizeof zero) != cudaSuccess)
     return WQ_ERR_CUDA;
-  if (cudaMemcpyFromSymbol(&cache_word, wq::g_cache_error_word, sizeof cache_word) != cudaSuccess)
-    return WQ_ERR_CUDA;
-  if (cache_word != 0 &&
-      cudaMemcpyToSymbol(wq::g_cache_error_word, &zero, sizeof zero) != cudaSuccess)
-    return WQ_ERR_CUDA;
-  word |= cache_word;
   if (flags) *flags = word;
   if (word & WQ_DEVICE_ERR_TIMEOUT) return WQ_ERR_TIMEOUT;
   if (word) return WQ_ERR_DEVICE;

@@ -17,16 +17,15 @@
 
 namespace wq {
 
-// Device error bits of the cache operators.  A word of their own: the GEMM's waits
-// look at g_error_word and would give up on any bit in it.
+// Device error bits of the cache operators, in the second error word: the GEMM's waits
+// would give up on any bit in the first.
 enum : unsigned { kErrCache = 4u };
-__device__ unsigned int g_cache_error_word = 0u;
 
 namespace {
 
 constexpr int kBlockTokens = 16;
 
-__device__ __forceinline__ void raise_cache_error() { atomicOr(&g_cache_error_word, kErrCache); }
+__device__ __forceinline__ void raise_cache_error() { atomicOr(&g_error_words[1], kErrCache); }
 
 // The sequence that packed row r belongs to: the last b with start[b] <= r, found 32
 // candidates at a time by a whole warp; -1 if r is before the first or behind the last

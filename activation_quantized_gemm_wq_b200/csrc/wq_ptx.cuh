@@ -8,8 +8,9 @@
 
 namespace wq {
 
-// Device-side error word.  Bounded waits that give up OR a bit in here; the
-// host reads (and clears) it with wq_device_status().
+// Device-side error words.  Bounded waits that give up OR a bit in the first, which the
+// GEMM's other waits look at; what must not stop those (wq_kv8.cuh's table checks) goes to
+// the second.  The host reads (and clears) both with wq_device_status(), in one copy.
 enum : unsigned {
   kErrWaitTimeout = 1u,   // an mbarrier wait exceeded its time limit
   kErrBadStreamId = 2u,   // a stream id >= S was seen (checked by the quantizer)
@@ -17,7 +18,7 @@ enum : unsigned {
 
 // Defined here: the library is compiled as a single translation unit
 // (wq_api.cu includes every kernel file), so there is exactly one copy.
-__device__ unsigned int g_error_word = 0u;
+__device__ unsigned int g_error_words[2] = {0u, 0u};
 
 // A wait gives up after this many nanoseconds of %globaltimer time.  Every
 // legitimate wait in these kernels lasts microseconds.
@@ -41,10 +42,10 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
 }
 
 __device__ __forceinline__ bool error_raised() {
-  return *reinterpret_cast<volatile unsigned int*>(&g_error_word) != 0u;
+  return *reinterpret_cast<volatile unsigned int*>(&g_error_words[0]) != 0u;
 }
 
-__device__ __forceinline__ void raise_error(unsigned bits) { atomicOr(&g_error_word, bits); }
+__device__ __forceinline__ void raise_error(unsigned bits) { atomicOr(&g_error_words[0], bits); }
 
 // ----------------------------------------------------------------- mbarrier
 

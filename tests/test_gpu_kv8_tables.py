@@ -112,3 +112,23 @@ def test_append_of_a_value_that_is_not_finite_is_seen(t, bad, D):
     wq.wq_kv8_append(x["k"][:n], x["v"][:n], ints([0, n]), ints([0]), table, **got)
     assert bool(got[t + "_scale"][hit, 1, 1].isfinite())
     assert wq.wq_device_status() == ("WQ_OK", 0)
+
+
+def test_both_error_words_are_read_and_cleared_together():
+    """A stream id outside the table and a bad row table, then neither."""
+    table, pages = page_table([ROOM], PAGE)
+    cache = random_cache(pages, HEADS, PAGE, D, 6)
+    x = torch.randn(T, HEADS, D, device="cuda").bfloat16()
+    K = HEADS * D
+    ids = torch.tensor([0] * (T - 1) + [5], dtype=torch.uint8, device="cuda")
+    quantized = (torch.empty(T, K, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda"))
+
+    def quantize(stream_id):
+        wq.wq_act_quant(x.view(T, K), torch.ones(K, device="cuda"), stream_id,
+                        torch.ones(1, 3, device="cuda"), 0, 8, *quantized)
+
+    for rows, stream_id, flags in (([9, 12], ids, 6), ([0, 8], ids, 2), ([9, 12], ids * 0, 4)):
+        wq.wq_kv8_append(x, x, ints(rows), ints([0]), table, **cache)
+        quantize(stream_id)
+        assert wq.wq_device_status() == ("WQ_ERR_DEVICE", flags)
+        assert wq.wq_device_status() == ("WQ_OK", 0)
