@@ -180,8 +180,10 @@ def _stream(stream):
         global _raw_stream
         if _raw_stream is None:
             import torch
-            # the raw handle alone: building a torch Stream object costs as much as a launch
-            _raw_stream = torch._C._cuda_getCurrentRawStream
+            # the raw handle alone, where this torch has the (undocumented) call: building a
+            # torch Stream object costs as much as a launch
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
         return _raw_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
