@@ -260,11 +260,11 @@ __device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t h) {
   return pack_half2(a - f.x, b - f.y);
 }
 
-// 2^n for a whole n below 128, exactly; 0 below the subnormals.
-__device__ __forceinline__ float exp2_whole(float n) {
-  const int e = static_cast<int>(fmaxf(n, -150.0f));
-  return __uint_as_float(e >= -126 ? static_cast<uint32_t>(e + 127) << 23
-                                   : e >= -149 ? 1u << (e + 149) : 0u);
+// 2^x down to the smallest subnormal.
+__device__ __forceinline__ float exp2_full(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float log2_approx(float x) {  // -infinity for subnormals
@@ -568,15 +568,26 @@ __device__ __forceinline__ int slab_offset(int row, int d) {
   return row * D + (((d >> 2) ^ (row & 7)) << 2);
 }
 
-// The end of a segment: the warps' sums are joined relative to the largest maximum, in
+// What the warps leave of a segment in shared memory: their rows' references, sums of
+// weights, and exponents of sums of p v.
+template <int RT>
+struct AttnRows {
+  float m[kAttnWarps][RT], l[kAttnWarps][RT], me[kAttnWarps][RT];  // me: m + e
+  const float* slab[kAttnWarps];                                  // the sums of p v themselves
+
+  __device__ __forceinline__ void put(int warp, int r, const AttnRow& row, float sum) {
+    m[warp][r] = row.m;
+    l[warp][r] = sum;
+    me[warp][r] = row.m + row.exponent();
+  }
+};
+
+// The end of a segment: the warps' sums are joined relative to the largest reference, in
 // order, and written as the result, or as a partial one where other CTAs have a part of the
-// item; rows [row0, row0 + ROWS) of a tile of RT.  In shared memory: row_m, row_l [warp][row]
-// maxima and sums of the warps' rows, slabs[warp] their outputs of these rows, already
-// relative to that maximum and in units of 1 / kSumUnit.
-template <int D, int RT, int ROWS>
+// item; rows [row0, row0 + ROWS) of a tile of RT, in PARTS rows of a slab each.
+template <int D, int RT, int ROWS, int PARTS>
 __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw,
-                                            const float (*row_m)[RT], const float (*row_l)[RT],
-                                            const float* const* slabs, int r_first, int row0,
+                                            const AttnRows<RT>& left, int r_first, int row0,
                                             int head, bool whole, bool from_start) {
   constexpr int WT = kAttnWarps;
   const int G = a.q_heads / a.kv_heads, rows = sw.nq * G;
@@ -587,13 +598,23 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
     if (r_first + r >= rows) break;
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k][r]);
+    for (int k = 0; k < WT; ++k) top = fmaxf(top, left.m[k][r]);
+    const float ref = top == -INFINITY ? 0.0f : top;
     float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
     for (int k = 0; k < WT; ++k) {
-      sum += row_l[k][r] * exp2_whole(row_m[k][r] - top);  // (a warp without tokens: 0 * 0)
-      const float4 p = *reinterpret_cast<const float4*>(slabs[k] + slab_offset<D>(r - row0, d));
-      v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+      sum += left.l[k][r] * exp2_approx(left.m[k][r] - ref);  // (a warp without tokens: 0 * 0)
+      // (kOutUnit and f one after the other: their quotient may be below the range)
+      const float f = exp2_full(left.me[k][r] - ref);
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) {
+        const float4 p = *reinterpret_cast<const float4*>(
+            left.slab[k] + slab_offset<D>(r - row0 + part * ROWS, d));
+        v.x = fmaf(p.x * (1.0f / kOutUnit), f, v.x);
+        v.y = fmaf(p.y * (1.0f / kOutUnit), f, v.y);
+        v.z = fmaf(p.z * (1.0f / kOutUnit), f, v.z);
+        v.w = fmaf(p.w * (1.0f / kOutUnit), f, v.w);
+      }
     }
     if (whole) {
       const float inv = sum > 0.0f ? kOutUnit / sum : 0.0f;
@@ -656,8 +677,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t full[WT][STAGES];
-  __shared__ float row_m[WT][RT], row_l[WT][RT];
-  __shared__ const float* slab_at[WT];
+  __shared__ AttnRows<RT> left;
   __shared__ AttnSched sched;
 
   const int wt = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -947,47 +967,33 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
         float l = row[mt][h].l;
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-        if (t == 0) {
-          row_m[wt][16 * mt + 8 * h + g] = row[mt][h].m;
-          row_l[wt][16 * mt + 8 * h + g] = l;
-        }
+        if (t == 0) left.put(wt, 16 * mt + 8 * h + g, row[mt][h], l);
       }
     // on to the next segment: its first copies go to the stage `phase` names, this one's sums
     // to the others of the warp's own ring, whose stages have all been read
     const bool whole = seg.whole(), from_start = j0 == 0;
     const bool more = seg.advance(a, sched) && __all_sync(0xFFFFFFFFu, dead < 0);
     float* slab = reinterpret_cast<float*>(my_ring + (phase + 1) % STAGES * STEP);
-    if (lane == 0) slab_at[wt] = slab;
+    if (lane == 0) left.slab[wt] = slab;
     if (more) {
       seg.begin(a);
       if (seg.count > 0) issue(0, 0);
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      __syncthreads();
+      if (mt > 0) __syncthreads();  // the slabs have been read
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 8 * h + g;
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < WT; ++i) top = fmaxf(top, row_m[i][16 * mt + r]);
-        const AttnRow& mine = row[mt][h];
-        const float fade =
-            mine.m == -INFINITY ? 0.0f : exp2_whole(mine.m - top + mine.exponent());
-#pragma unroll
-        for (int nd = 0; nd < ND; ++nd)  // (kSumUnit / 2^kPShift times fade may be below the range)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) o[mt][nd][2 * h + e] *= 1.0f / kOutUnit;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int nd = 0; nd < ND; nd += 4)
-            *reinterpret_cast<float4*>(slab + slab_offset<D>(r, t * (D / 4) + part * ND + nd)) =
-                make_float4(o[mt][nd][2 * h + part] * fade, o[mt][nd + 1][2 * h + part] * fade,
-                            o[mt][nd + 2][2 * h + part] * fade, o[mt][nd + 3][2 * h + part] * fade);
-      }
+            *reinterpret_cast<float4*>(slab +
+                                       slab_offset<D>(8 * h + g, t * (D / 4) + part * ND + nd)) =
+                make_float4(o[mt][nd][2 * h + part], o[mt][nd + 1][2 * h + part],
+                            o[mt][nd + 2][2 * h + part], o[mt][nd + 3][2 * h + part]);
       __syncthreads();
-      attn_finish<D, RT, 16>(a, sw, row_m, row_l, slab_at, r_first, 16 * mt, head, whole, from_start);
+      attn_finish<D, RT, 16, 1>(a, sw, left, r_first, 16 * mt, head, whole, from_start);
     }
     // the next copies write where the sums were written and read by ordinary accesses
     fence_proxy_async_smem();
@@ -1029,7 +1035,7 @@ struct AttnFewCfg {
   static constexpr int RING = WT * STAGES * STEP;
   static constexpr int SMEM = RING + 1024;            // + alignment
   static constexpr int CTAS = D == 128 ? 3 : 4;
-  static_assert(RT * D * 4 <= STEP, "a warp's sums fit one stage");
+  static_assert(8 * D * 4 <= STEP, "a warp's sums, in eight columns, fit one stage");
 };
 
 template <int D, int RT_>
@@ -1044,8 +1050,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t full[WT][STAGES];
-  __shared__ float row_m[kAttnWarps][RT], row_l[kAttnWarps][RT];
-  __shared__ const float* slab_at[kAttnWarps];
+  __shared__ AttnRows<RT> left;
   __shared__ AttnSched sched;
 
   const int wt = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -1216,11 +1221,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
           u = fmaxf(u, __shfl_xor_sync(0xFFFFFFFFu, u, x));
         }
         const float fade = row.raise(top, u);
-        const float f0 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t);
-        const float f1 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4);
+        if (i > 0) {  // (at the first step nothing has been summed)
+          const float f0 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t);
+          const float f1 = __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4);
 #pragma unroll
-        for (int x = 0; x < MD; ++x) {
-          o[x][0] *= f0; o[x][1] *= f1; o[x][2] *= f0; o[x][3] *= f1;
+          for (int x = 0; x < MD; ++x) {
+            o[x][0] *= f0; o[x][1] *= f1; o[x][2] *= f0; o[x][3] *= f1;
+          }
         }
       }
       const float base = row.base();
@@ -1284,10 +1291,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
     float l = row.l;
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    if (t == 0 && g < RT) {
-      row_m[wt][g] = row.m;
-      row_l[wt][g] = l;
-    }
+    if (t == 0 && g < RT) left.put(wt, g, row, l);
     // on to the next segment: its first copies go to the stage `phase` names, this one's
     // sums to the other (of the warp's own ring, whose stages have all been read)
     const bool whole = seg.whole(), from_start = j0 == 0;
@@ -1297,33 +1301,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
       seg.begin(a);
       if (seg.count > 0) issue(0, 0);
     }
-    __syncthreads();
-    float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < WT; ++k) top = fmaxf(top, row_m[k][FOUR ? g & 3 : g]);
-    const float fade = row.m == -INFINITY ? 0.0f : exp2_whole(row.m - top + row.exponent());
-    const float fq[2] = {__shfl_sync(0xFFFFFFFFu, fade, 8 * t), __shfl_sync(0xFFFFFFFFu, fade, 8 * t + 4)};
-    if constexpr (FOUR) {  // the two parts
-#pragma unroll
-      for (int x = 0; x < MD; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[x][e] += __shfl_xor_sync(0xFFFFFFFFu, o[x][e], 2);
-    }
-#pragma unroll
-    for (int x = 0; x < MD; ++x)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[x][e] *= 1.0f / kOutUnit;  // (times fade may be below the range)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (2 * t + e >= RT) break;
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int x = 0; x < MD; x += 2)
         *reinterpret_cast<float4*>(slab + slab_offset<D>(2 * t + e, g * (D / 8) + 2 * x)) =
-            make_float4(o[x][e] * fq[e], o[x][2 + e] * fq[e], o[x + 1][e] * fq[e], o[x + 1][2 + e] * fq[e]);
-    }
-    if (lane == 0) slab_at[wt] = slab;
+            make_float4(o[x][e], o[x][2 + e], o[x + 1][e], o[x + 1][2 + e]);
+    if (lane == 0) left.slab[wt] = slab;
     __syncthreads();
-    attn_finish<D, RT, RT>(a, sw, row_m, row_l, slab_at, r_first, 0, head, whole, from_start);
+    attn_finish<D, RT, RT, FOUR ? 2 : 1>(a, sw, left, r_first, 0, head, whole, from_start);
     // the next copies write where the sums were written and read by ordinary accesses
     fence_proxy_async_smem();
     if (__syncthreads_or(dead >= 0)) {  // the error word is set
