@@ -342,10 +342,10 @@ struct GemvCfg {
 // [part] 2 KB per column tile, [word j][column][t][8 channels].
 //
 // Measured (calls in a graph, nothing in L2): 1 token, 2048 x 2048, groups of 128, 4.1 us;
-// 1 token, 4096 -> 12288, 8.1 us, 3.2 TB/s, of which the stream is 4 to 5 us and the rest the
+// 1 token, 4096 -> 12288, 8.2 us, 3.2 TB/s, of which the stream is 4 to 5 us and the rest the
 // start (the tokens, the scales, the first stage) and the joining; 8 tokens, 16384 -> 4096,
 // groups of 64, cinv, 19.5 us, 1.8 TB/s (18.9 us with 11 bits of x * cinv); 16 tokens,
-// 8192 -> 8191, groups of 32, 22.5 us, 1.7 TB/s: there the staging of the tokens in every CTA,
+// 8192 -> 8191, groups of 32, 22.4 us, 1.7 TB/s, with cinv 32.7 us (24.3 us with 11 bits): there the staging of the tokens in every CTA,
 // the conversions and the exchange count, not the copies.  Weights loaded straight into
 // registers, without the rings, took 2.8 us for the first, whose warps have one stage or two,
 // but 12.3 us for the second and 40 and 28 us for the last two.

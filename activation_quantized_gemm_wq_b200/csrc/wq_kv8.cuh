@@ -73,7 +73,7 @@ struct AppendArgs {
 // one row for decoding (a warp per new token) and 16 rows for long runs (about one block
 // per warp, and no warps that find nothing).  The issue of instructions (54 % of cycles; about
 // 650 for a block) and the latency of a block's loads bound it: 3 sequences of up to 4256
-// tokens, 32 heads of 128, 54.9 us, 4.2 TB/s read and written; 32 single tokens, 8 heads,
+// tokens, 32 heads of 128, 55.1 us, 4.2 TB/s read and written; 32 single tokens, 8 heads,
 // 3.3 us.  Exact quotients by two remainder steps, without a test for near ties, and 32-bit
 // indices within a page took the first from 109 to 60 us, five CTAs to an SM below 55.
 template <int D>
@@ -643,13 +643,16 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const SeqWork& sw
 // segment is fetched while a segment's sums are joined.  Codes become f16 in registers,
 // exactly (with MT = 2 once for 32 query rows); q enters as f16 after a power-of-two scaling
 // per row that keeps all its 8 bits; scores, maxima, sums and the output are fp32.  Block
-// scales multiply the scores (keys) and the softmax weights relative to a power-of-two
-// reference (values).
-// Eight warps to an SM (247 registers) issue in a third of all cycles: the chain of copies'
-// arrival, conversion, matrix steps and softmax bounds it, not the tensor cores (22 %) nor
-// memory (11 %).  2 x 64 queries over up to 8512 tokens, 32 heads of 64: 55.2 us (58.1 with
-// MT = 1, 83.5 with the first, simple kernel).  Making the codes f16 once per CTA in shared
-// memory for 64 rows was 3 % faster there, but 4 to 7 % slower for heads of 128.
+// scales multiply the scores (keys) and the softmax weights, relative to their row's
+// power-of-two reference (values).
+// Eight warps to an SM (255 registers) issue in 37 % of all cycles: the chain of copies'
+// arrival, conversion, matrix steps and softmax bounds it, not the tensor cores (28 %) nor
+// memory (10 %).  2 x 64 queries over up to 8512 tokens, 32 heads of 64: 64.2 us, of 128:
+// 100.8 us; 2 x 256 queries, heads of 128: 257 us.  The weights' second parts, half as many
+// matrix steps again, are most of what these took less without them (57.3, 84 and 210 us; 55.2,
+// 82.2 and 204 us with one reference to a warp).  With one part: 58.1 us for the first with
+// MT = 1 (83.5 us the first, simple kernel); codes made f16 once per CTA in shared memory for
+// 64 rows were 3 % faster there, but 4 to 7 % slower for heads of 128.
 template <int D, int MT>
 struct AttnCfg {
   static constexpr int WT = kAttnWarps;
@@ -1024,9 +1027,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnCfg<D, MT>::CTAS) attn_kv
 // are joined (in the other stage of each warp's ring).
 // Long contexts are bound by memory, after about 10 us of start, segments' ends and joining:
 // one token each, four query heads to a cache head of 128: 32 sequences of up to 8192 tokens
-// 60.7 us, 5.2 TB/s; 2 of up to 131072 71.0 us, 5.3 TB/s; 8 of 131072 reach 6.2 TB/s.  A single
-// sequence of up to 500 tokens, 16 heads, takes 9.0 us, all of it latency.  (The first, simple
-// kernel: 84.0, 87.6 and 11.1 us.)
+// 61.6 us, 5.1 TB/s; 2 of up to 131072 71.5 us, 5.2 TB/s; 8 of 131072 reach 6.2 TB/s.  A single
+// sequence of up to 500 tokens, 16 heads, takes 9.4 us, all of it latency.  (The first, simple
+// kernel: 84.0, 87.6 and 11.1 us; before weights had a second part and rows a reference of their
+// own: 61.0, 71.3 and 9.0 us.)  Eight query heads to a cache head, 16 sequences of up to 8192
+// tokens, four heads of 128: 27.9 us, 2.5 TB/s.
 template <int D, int RT_>
 struct AttnFewCfg {
   static constexpr int RT = RT_, WT = kAttnWarps, TILE = kBlockTokens * D;
@@ -1328,7 +1333,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, AttnFewCfg<D, RT_>::CTAS) att
 // one four of outputs, so that every load is in flight at once; they are added as a tree, the
 // same every time.  Latency bounds it: with one thread to an output, its parts one after the
 // other, 2 x 131072 tokens took 83.9 us in all instead of 73.  Sixteen CTAs to an end of tiles
-// of 32 rows of 64 channels: 57.3 us for the chunk of 64 queries instead of 55.1 with four.
+// of 32 rows of 64 channels: 69 us for two chunks of 64 queries instead of 64 with four; four to
+// those of 128 channels 104 instead of 101 with twelve.
 constexpr int join_split(int RT, int D) { return RT * D >= 4096 ? 12 : 4; }
 
 template <int D>
@@ -1394,7 +1400,8 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnArgs a, in
 
 // Rows of a tile, by the rows per cache head that an average sequence has: 4 or 8 (their
 // own kernel), 16 or 32.  (64 rows on pairs of warps that shared their copies lost to two
-// tiles of 32 everywhere: 57.9 / 54.4 us for chunks of 64 over 8512 tokens, heads of 64.)
+// tiles of 32 everywhere: 57.9 / 54.4 us for chunks of 64 over 8512 tokens, heads of 64, with
+// weights of one part.)
 int attn_tile_rows(int Tq, int B, int q_heads, int kv_heads) {
   const long long rows = static_cast<long long>(Tq) * (q_heads / kv_heads);
   return rows <= 4LL * B ? 4 : rows <= 8LL * B ? 8 : rows <= 16LL * B ? 16 : 32;
@@ -1402,9 +1409,9 @@ int attn_tile_rows(int Tq, int B, int q_heads, int kv_heads) {
 
 // Whether items are left whole, one CTA each, and the joining kernel is not launched: where
 // the tables have room for few tokens, or for not many and there are items for every SM.
-// Measured whole / cut, us: 16 items of at most 512 tokens 9.0 / 10.1, 512 of them 21.6 / 36.5;
-// 512 of at most 1024 tokens 31.1 / 37.8, but 8 of them 12.7 / 10.9; 512 of at most 2048,
-// heads of 64 25.4 / 36.0, of 128 51.3 / 49.0.
+// Measured whole / cut, us: 16 items of at most 512 tokens 9.4 / 9.6, 512 of them 23.1 / 36.1;
+// 512 of at most 1024 tokens 33.3 / 37.6, but 8 of them 13.6 / 10.1; 512 of at most 2048,
+// heads of 64 28.4 / 37.1, of 128 54.7 / 48.8.
 bool attn_whole(const Kv8Cache& c, int Tq, int q_heads, int RT) {
   const long long tokens = static_cast<long long>(c.max_pages) * c.page_tokens;
   const long long rows = static_cast<long long>(Tq) * (q_heads / c.kv_heads);

@@ -82,10 +82,11 @@ typedef enum {
 const char* wq_status_string(wq_status s);
 
 /* ABI version of this library (major * 100 + minor; the minor number grows when
- * entry points of the fused linear are added, the major one when an existing
- * signature or contract changes).  101: adds wq_gemm_plan_query.  The operators
- * beside the linear (wq_pack_int4_group, wq_gemv_w4g, wq_kv8_append, wq_attn_kv8)
- * leave it as it is; a caller that may meet an older library looks up the symbol. */
+ * entry points are added, the major one when an existing signature or contract
+ * changes).  101: adds wq_gemm_plan_query.  One exception: wq_pack_int4_group,
+ * wq_gemv_w4g, wq_kv8_append, wq_attn_kv8, wq_attn_kv8_workspace_bytes and
+ * WQ_DEVICE_ERR_CACHE came without a new number, so 101 does not tell whether a
+ * library has them; a caller that may meet an older one looks up the symbol. */
 int wq_version(void);
 
 /* Bytes of device workspace wq_linear_w4a8 / wq_linear_w4a4 need for M token
@@ -405,16 +406,15 @@ wq_status wq_gemv_w4g(const wq_bf16* x, int M, int K, int N, const float* cinv,
  *                                        before past_len[b], else 0
  *   new code = clamp(rint_half_even(x / s_new), -127, 127), 0 where s_new is 0
  *   old code = rint_half_even(old code * (s_old / s_new))   where s_new > s_old
- * (a value that is not finite makes s_new NaN, and a block with such a scale keeps it:
- * its keys or values are not finite to the queries that see them)
  * in IEEE fp32: the scale is that of the largest value in the block, however the tokens
  * came; a token costs at most half a step when it is written and half a step each time
- * a later token of its block raises the scale.  Slots behind the new tokens keep their
- * contents.
+ * a later token of its block raises the scale.  A value that is not finite makes s_new
+ * NaN, which the block keeps: its keys or values are not finite to the queries that see
+ * them.  Slots behind the new tokens keep their contents.
  * Checked on the device: 0 <= past_len, the tokens fit max_pages, the pages used are in
  * [0, pages), row_start does not decrease and stays within [0, T].  A violation sets
  * WQ_DEVICE_ERR_CACHE; nothing is written for a sequence that does not fit or whose rows
- * lie outside [0, T], nor to a page outside the cache. */
+ * lie outside [0, T], nor to a page outside the cache.  (T or B of 0 returns at once.) */
 wq_status wq_kv8_append(const wq_bf16* k, const wq_bf16* v, int64_t k_stride, int64_t v_stride,
                         int T, const int32_t* row_start, const int32_t* past_len, int B,
                         const int32_t* block_table, int max_pages, int8_t* k_codes,
@@ -443,13 +443,13 @@ size_t wq_attn_kv8_workspace_bytes(int Tq, int B, int q_heads, int kv_heads, int
  * Scores, softmax and sums are fp32; values of q below 2^-21 of their row's largest (one
  * query, one head) are off by at most 2^-30 of it, the others exact; the products of
  * softmax weights and value scales are held to 2^-22 of themselves or 2^-35 of their row's
- * largest.  For the same arguments the result
- * is the same on every call; calls that may run at the same time need workspaces of
- * their own.  Work is shared out from kv_len and q_start as they are on the device, so a
- * captured call may be replayed after they changed.
+ * largest.  For the same arguments the result is the same on every call; calls that may
+ * run at the same time need workspaces of their own.  Work is shared out from kv_len and
+ * q_start as they are on the device, so a captured call may be replayed after they changed.
  * Checked on the device: kv_len in [0, max_pages * page_tokens], pages in [0, pages),
- * q_start as row_start above.  A violation sets WQ_DEVICE_ERR_CACHE; lengths are then cut
- * to their range and a bad page is read as page 0. */
+ * q_start as row_start above (Tq or B of 0 returns at once).  A violation sets
+ * WQ_DEVICE_ERR_CACHE; lengths are then cut to their range and a bad page is read as page
+ * 0. */
 wq_status wq_attn_kv8(const wq_bf16* q, int64_t q_stride, int Tq, int q_heads,
                       const int32_t* q_start, const int32_t* kv_len, int B,
                       const int32_t* block_table, int max_pages, const int8_t* k_codes,
